@@ -336,6 +336,180 @@ int va_merge(const float* o_part, const float* lse_part, int S, int B, int T, in
  */
 int va_verify_attn_noalloc(const va_attn_args* args, va_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Around the verify call: the drafter's and the target's logits, and the
+ * eviction of cached keys.  The pages have no counterpart of these calls.
+ * ---------------------------------------------------------------------- */
+
+/* Arguments of va_token_logprobs.  Zero-initialise, then fill. */
+typedef struct va_logprob_args {
+  int dtype;              /* VA_F32 or VA_BF16 logits                             */
+  int R, V;               /* rows, vocabulary size (V >= 1)                       */
+  long long ld;           /* elements from one row to the next, >= V              */
+  float scale;            /* finite, > 0: logits are multiplied by it (1 / temperature) */
+  const void* logits;     /* [device] [R, ld] dtype, aligned to an element; only
+                             the first V of a row are read                        */
+  const int32_t* tokens;  /* [device] [R, G]: given tokens, < 0 = none; NULL if G == 0 */
+  int G;                  /* given tokens per row, 0 .. 65536                     */
+  int K;                  /* top alternatives per row, 0 .. VA_MAX_TOPK, <= V     */
+  float* lse;             /* [device] [R]    nullable: ln sum_v exp(scale x_v)    */
+  float* entropy;         /* [device] [R]    nullable: -sum_v p_v ln p_v          */
+  float* tok_lp;          /* [device] [R, G] log probability of the given tokens
+                             (-inf for a token < 0); required when G > 0          */
+  int32_t* top_ids;       /* [device] [R, K] the K largest logits, descending, equal
+                             ones by lower index; required when K > 0             */
+  float* top_lp;          /* [device] [R, K] nullable: their log probabilities    */
+  double* top_lp64;       /* [device] [R, K] nullable: the same values widened, the
+                             type va_build_tree reads                             */
+  int32_t* row_status;    /* [device] [R] nullable: VA_ERR_INVALID_ARG for a row with
+                             a NaN or +inf logit (its values come out as NaN, its
+                             ids as -1) or a token >= V (that token's value is
+                             NaN); entries of other rows are not written          */
+} va_logprob_args;
+
+/*
+ * Log probabilities of given tokens, entropy and top alternatives of each row
+ * of logits, in one pass over them.  The drafter's side of the step: with R =
+ * B * L and K = the tree's width it makes the (lp, tok) that va_build_tree
+ * reads; the target's side: with R = B * T and K = 1, top_ids is the
+ * target_next that va_tree_accept reads.
+ *   lse = ln sum_v exp(scale x_v)        lp_v = scale x_v - lse
+ *   entropy = -sum_v exp(lp_v) lp_v      (0 ln 0 = 0)
+ * Sums are held in fp32.  -inf logits (masked tokens) have log probability
+ * -inf and rank behind all finite ones; a row of nothing but -inf has lse
+ * -inf, entropy 0, log probabilities -inf and the K lowest ids.  Equal logits
+ * compare as they are stored, before scaling, and +0 equals -0.
+ * R >= 0; no workspace.  A top_ids or top_lp row is dense, [K].
+ */
+int va_token_logprobs(const va_logprob_args* args, va_stream_t stream);
+
+/* Arguments of va_key_weights.  Zero-initialise, then fill.  The fields up to
+ * tree_mask, flags and kv_scale are va_attn_args' and mean the same; H T
+ * queries, cache and mask are those of the verify call that returned lse. */
+typedef struct va_key_weight_args {
+  int dtype;
+  int B, H, T;
+  float scale;
+  const void* q_nope;
+  const void* q_pe;
+  const void* c_kv;
+  const void* k_pe;
+  int num_pages;
+  int page_size;
+  const int32_t* page_table;
+  int max_pages;
+  const int32_t* kv_len;
+  const uint64_t* tree_mask;
+  const float* lse;          /* [device] [B, T, H] from va_verify_attn            */
+  const int32_t* path;       /* [device] [B, T] nullable: only the nodes
+                                path[b][0 .. accept_len[b]) count (va_tree_accept);
+                                NULL: every node counts                           */
+  const int32_t* accept_len; /* [device] [B], with path                           */
+  const float* weights_in;   /* [device] [B, 64 max_pages] nullable: the weights
+                                so far (NULL: zeros)                              */
+  float decay;               /* finite: multiplies weights_in                     */
+  float* weights;            /* [device] [B, 64 max_pages] out; may be weights_in */
+  int32_t* req_status;       /* [device] [B] nullable, see below                  */
+  void* workspace;           /* [device] >= va_key_weights_workspace_bytes(),
+                                256-byte aligned                                  */
+  size_t workspace_bytes;
+  int flags;                 /* VA_FLAG_BF16_CUDA_CORES, VA_FLAG_KV_FP8_E4M3      */
+  float kv_scale;
+} va_key_weight_args;
+
+/* Workspace needed by va_key_weights for these arguments (0: none, or bad
+ * arguments).  It depends on the sizes and the device, not on array contents. */
+size_t va_key_weights_workspace_bytes(const va_key_weight_args* args);
+
+/*
+ * Accumulated attention weight of the cached keys: what va_evict_plan ranks
+ * them by.  The probabilities are recomputed from the verify call's lse, so
+ * nothing of size keys x rows is ever stored:
+ *   weights[b][j] = decay * weights_in[b][j]
+ *     + sum over counted nodes n and heads h, j visible to n, of
+ *       exp(scale * (q_nope . c_kv_j + q_pe . k_pe_j) - lse[b][n][h])
+ * for 0 <= j < kv_len[b]; entries from kv_len[b] on are not touched.  A node
+ * counts as often as path lists it; rows whose own mask bit is clear or whose
+ * lse is -inf (absent nodes) add nothing.  Products of bf16 queries run on
+ * tensor cores unless VA_FLAG_BF16_CUDA_CORES is given; sums are fp32, and
+ * their order, so every bit of the result, depends on sizes alone.
+ * req_status[b] becomes VA_ERR_INVALID_ARG when kv_len[b] is out of range
+ * (the request's weights are then not written), when accept_len[b] is outside
+ * [0, T] (nothing is added), or when a path entry or a page index is out of
+ * range (that node, or that page's keys, get nothing added), and VA_ERR_CUDA
+ * when a bounded wait expires (the weights are then unspecified); entries of
+ * requests without a problem are not written.
+ */
+int va_key_weights(const va_key_weight_args* args, va_stream_t stream);
+
+/* Arguments of va_evict_plan.  Zero-initialise, then fill. */
+typedef struct va_evict_args {
+  int B;
+  int capacity;              /* slots of a request: row stride of the arrays below */
+  int T;                     /* tree nodes at the end of the cache, 0 .. VA_MAX_QLEN;
+                                0: every cached key is a candidate                */
+  const float* weights;      /* [device] [B, capacity] (va_key_weights)           */
+  const int32_t* kv_len;     /* [device] [B] keys in the cache, T included        */
+  const int32_t* budget;     /* [device] [B] keys to keep                         */
+  const int32_t* path;       /* [device] [B, T] accepted nodes (va_tree_accept);
+                                required when T > 0                               */
+  const int32_t* accept_len; /* [device] [B], with path                           */
+  const int32_t* pos;        /* [device] [B, capacity] nullable: token position of
+                                each slot's key (NULL: the slot)                  */
+  int n_sink, n_recent;      /* >= 0: keys of position < n_sink, and the n_recent
+                                newest positions, are protected                   */
+  int32_t* new_len;          /* [device] [B] out: keys that stay                  */
+  int32_t* from_slot;        /* [device] [B, capacity] out: slot whose key ends up
+                                in this one; -1 from new_len on                   */
+  float* weights_out;        /* [device] [B, capacity] nullable out: the weights of
+                                the keys in their new slots, 0 from new_len on;
+                                may be weights                                    */
+  int32_t* pos_out;          /* [device] [B, capacity] nullable out, with pos: -1
+                                from new_len on; may be pos                       */
+  int32_t* req_status;       /* [device] [B] nullable                             */
+} va_evict_args;
+
+/*
+ * Eviction from the cache by accumulated attention weight, first half: which
+ * keys stay, and in which slots.  With P = kv_len[b] - T, the candidates are
+ * the prefix slots [0, P) and the slots P + path[b][i], i < accept_len[b] (the
+ * rejected nodes are always dropped, so a large budget makes this the commit
+ * of the accepted path).  Protected are the accepted nodes, the candidates
+ * whose position is below n_sink, and those with (largest position of a
+ * candidate) - position < n_recent.  All protected keys stay; of the others
+ * the heaviest, equal weights by lower slot, NaN like -inf, until
+ *   new_len = max(min(max(budget, 0), candidates), protected)
+ * keys stay.  Kept keys in slots below new_len stay where they are; the i-th
+ * slot below new_len that is not kept takes the i-th kept key from new_len on
+ * (both ascending).  Attention over the prefix does not depend on the order
+ * of its slots; pos follows each key when the caller needs its position.  So
+ * no slot is both read and written by the moves, and a plan may be applied to
+ * the caches of many layers, each in place (va_kv_move).
+ * req_status[b] becomes VA_ERR_INVALID_ARG when kv_len[b] is outside [T,
+ * capacity] (new_len 0, nothing stays in the plan), or when accept_len[b] is
+ * outside [0, T] or path[b] is not ascending within [0, T) (everything stays
+ * as it is: new_len = kv_len, from_slot the identity); entries of requests
+ * without a problem are not written.
+ */
+int va_evict_plan(const va_evict_args* args, va_stream_t stream);
+
+/*
+ * Second half: moves the keys of one cache as va_evict_plan says, in place.
+ *   c_kv [device] [num_pages, 64, 512], k_pe [device] [num_pages, 64, 64],
+ *        elements of elem_bytes (4: fp32, 2: bf16, 1: FP8 codes)
+ *   page_table [device] [B, max_pages]; its pages must belong to one request
+ *        each, up to that request's old length
+ *   from_slot [device] [B, 64 max_pages], new_len [device] [B]: of the plan
+ *   req_status [device] [B] nullable: VA_ERR_INVALID_ARG for a request whose
+ *        new_len is outside [0, 64 max_pages], or where a moved key's source is
+ *        not in [new_len, 64 max_pages) or its page index is out of range (that
+ *        key is not moved); entries of other requests are not written.
+ * Slots that no key moves to are not written.
+ */
+int va_kv_move(void* c_kv, void* k_pe, int elem_bytes, int num_pages, int page_size,
+               const int32_t* page_table, int B, int max_pages, const int32_t* from_slot,
+               const int32_t* new_len, int32_t* req_status, va_stream_t stream);
+
 /*
  * Diagnostic: number of bounded barrier waits inside the attention kernels
  * (the tensor-core kernel's pipeline barriers, the CUDA-core kernel's

@@ -13,7 +13,8 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional
+from contextlib import ExitStack, nullcontext
+from typing import Any, NamedTuple, Optional
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("VA_LIB", os.path.join(HERE, "libverifyattn.so"))
@@ -29,7 +30,8 @@ D_LATENT, D_ROPE, PAGE_SIZE, MAX_QLEN = 512, 64, 64, 65
 EXPORTS = ("va_max_qlen", "va_status_string", "va_build_tree", "va_build_tree_mask",
            "va_workspace_bytes", "va_num_splits", "va_verify_attn", "va_merge",
            "va_device_timeouts", "va_verify_attn_noalloc", "va_tree_accept",
-           "va_verify_attn_partials")
+           "va_verify_attn_partials", "va_token_logprobs", "va_key_weights_workspace_bytes",
+           "va_key_weights", "va_evict_plan", "va_kv_move")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 
@@ -48,6 +50,51 @@ class VaAttnArgs(ctypes.Structure):
         ("num_splits", ctypes.c_int), ("workspace", ctypes.c_void_p),
         ("workspace_bytes", ctypes.c_size_t), ("flags", ctypes.c_int),
         ("kv_scale", ctypes.c_float),
+    ]
+
+
+class VaLogprobArgs(ctypes.Structure):
+    """Mirror of ``va_logprob_args``."""
+
+    _fields_ = [
+        ("dtype", ctypes.c_int), ("R", ctypes.c_int), ("V", ctypes.c_int),
+        ("ld", ctypes.c_longlong), ("scale", ctypes.c_float), ("logits", ctypes.c_void_p),
+        ("tokens", ctypes.c_void_p), ("G", ctypes.c_int), ("K", ctypes.c_int),
+        ("lse", ctypes.c_void_p), ("entropy", ctypes.c_void_p), ("tok_lp", ctypes.c_void_p),
+        ("top_ids", ctypes.c_void_p), ("top_lp", ctypes.c_void_p), ("top_lp64", ctypes.c_void_p),
+        ("row_status", ctypes.c_void_p),
+    ]
+
+
+class VaKeyWeightArgs(ctypes.Structure):
+    """Mirror of ``va_key_weight_args``."""
+
+    _fields_ = [
+        ("dtype", ctypes.c_int), ("B", ctypes.c_int), ("H", ctypes.c_int), ("T", ctypes.c_int),
+        ("scale", ctypes.c_float),
+        ("q_nope", ctypes.c_void_p), ("q_pe", ctypes.c_void_p),
+        ("c_kv", ctypes.c_void_p), ("k_pe", ctypes.c_void_p),
+        ("num_pages", ctypes.c_int), ("page_size", ctypes.c_int),
+        ("page_table", ctypes.c_void_p), ("max_pages", ctypes.c_int),
+        ("kv_len", ctypes.c_void_p), ("tree_mask", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+        ("path", ctypes.c_void_p), ("accept_len", ctypes.c_void_p),
+        ("weights_in", ctypes.c_void_p), ("decay", ctypes.c_float), ("weights", ctypes.c_void_p),
+        ("req_status", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t), ("flags", ctypes.c_int), ("kv_scale", ctypes.c_float),
+    ]
+
+
+class VaEvictArgs(ctypes.Structure):
+    """Mirror of ``va_evict_args``."""
+
+    _fields_ = [
+        ("B", ctypes.c_int), ("capacity", ctypes.c_int), ("T", ctypes.c_int),
+        ("weights", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("budget", ctypes.c_void_p),
+        ("path", ctypes.c_void_p), ("accept_len", ctypes.c_void_p), ("pos", ctypes.c_void_p),
+        ("n_sink", ctypes.c_int), ("n_recent", ctypes.c_int),
+        ("new_len", ctypes.c_void_p), ("from_slot", ctypes.c_void_p),
+        ("weights_out", ctypes.c_void_p), ("pos_out", ctypes.c_void_p),
+        ("req_status", ctypes.c_void_p),
     ]
 
 
@@ -88,6 +135,16 @@ def load_library(path: Optional[str] = None):
     lib.va_verify_attn_noalloc.restype = I
     lib.va_verify_attn_partials.argtypes = [ctypes.POINTER(VaAttnArgs), I, I, V, V, V]
     lib.va_verify_attn_partials.restype = I
+    lib.va_token_logprobs.argtypes = [ctypes.POINTER(VaLogprobArgs), V]
+    lib.va_token_logprobs.restype = I
+    lib.va_key_weights_workspace_bytes.argtypes = [ctypes.POINTER(VaKeyWeightArgs)]
+    lib.va_key_weights_workspace_bytes.restype = Z
+    lib.va_key_weights.argtypes = [ctypes.POINTER(VaKeyWeightArgs), V]
+    lib.va_key_weights.restype = I
+    lib.va_evict_plan.argtypes = [ctypes.POINTER(VaEvictArgs), V]
+    lib.va_evict_plan.restype = I
+    lib.va_kv_move.argtypes = [V, V, I, I, I, V, I, I, V, V, V, V]
+    lib.va_kv_move.restype = I
     if path is None:
         _lib = lib
     return lib
@@ -256,7 +313,8 @@ def verify_attn_partials(args: VaAttnArgs, split_first: int, split_count: int, o
     lse_part float [count, B, T, H] (cuda tensors), no merge."""
     _check(load_library().va_verify_attn_partials(ctypes.byref(args), split_first, split_count,
                                                   _ptr(o_part), _ptr(lse_part), _stream(stream)),
-           "va_verify_attn_partials")
+           "va_verify_attn_partials", "va_token_logprobs", "va_key_weights_workspace_bytes",
+           "va_key_weights", "va_evict_plan", "va_kv_move")
 
 
 def merge(o_part, lse_part, out_dtype, stream=None):
@@ -269,3 +327,244 @@ def merge(o_part, lse_part, out_dtype, stream=None):
     _check(load_library().va_merge(_ptr(o_part.contiguous()), _ptr(lse_part.contiguous()), S, B, T,
                                    H, dt, _ptr(out), _ptr(lse), _stream(stream)), "va_merge")
     return out, lse
+
+
+# --------------------------------------------------------------------------
+# Around the verify call: logits, and the eviction of cached keys.  These
+# calls check the tensors they take (device, type, shape, density); the
+# library checks the rest.  What they allocate belongs to the stream that
+# they run on.
+
+def _on(t, stream):
+    """Context in which t's device and the given stream are the current ones."""
+    import torch
+    if stream is None and t.device.index == torch.cuda.current_device():
+        return nullcontext()
+    ctx = ExitStack()
+    ctx.enter_context(torch.cuda.device(t.device))
+    if stream is not None:
+        if stream.device != t.device:
+            raise VerifyAttnError(f"stream of {stream.device} for tensors on {t.device}")
+        ctx.enter_context(torch.cuda.stream(stream))
+    return ctx
+
+
+def _need(t, name: str, like, dtypes, shape):
+    """One tensor argument: cuda, on like's device, one of dtypes, dense, of this shape."""
+    if t.device != like.device or t.device.type != "cuda":
+        raise VerifyAttnError(f"{name} is on {t.device}: cuda tensors of one device are needed")
+    if t.dtype not in dtypes:
+        raise VerifyAttnError(f"{name} is {t.dtype}, not {' or '.join(str(d) for d in dtypes)}")
+    if t.shape != shape:
+        raise VerifyAttnError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if not t.is_contiguous():
+        raise VerifyAttnError(f"{name} is not contiguous")
+    return t.data_ptr()
+
+
+class TokenLogprobs(NamedTuple):
+    """What token_logprobs returns (None for what was not asked for)."""
+
+    lse: Any       # float32 [...]
+    entropy: Any   # float32 [...]
+    tok_lp: Any    # float32, tokens' shape
+    top_ids: Any   # int32 [..., k]
+    top_lp: Any    # float32 or float64 [..., k]
+
+
+def token_logprobs(logits, tokens=None, *, k: int = 0, scale: float = 1.0, wide: bool = False,
+                   row_status=None, stream=None) -> TokenLogprobs:
+    """Log-sum-exp, entropy, log probabilities of given tokens and top-k of rows of logits.
+
+    logits float32 or bfloat16 [..., V] (cuda; dense or a slice [..., :V] of padded
+    rows), scaled by `scale` (1 / temperature).  tokens int32 [...] or [..., G]: given
+    tokens, < 0 for none.  k <= 16 alternatives, equal logits by lower index; with
+    `wide` their log probabilities are float64, as build_tree reads them:
+    ``build_tree(r.top_lp, r.top_ids, budget)`` for drafter logits [B, L, V], and
+    ``tree_accept(parents, tokens, r.top_ids[..., 0])`` for target logits [B, T, V]
+    with k = 1."""
+    import torch
+    if logits.device.type != "cuda":
+        raise VerifyAttnError(f"logits are on {logits.device}: cuda tensors are needed")
+    if logits.dtype not in (torch.float32, torch.bfloat16):
+        raise VerifyAttnError(f"logits are {logits.dtype}, not float32 or bfloat16")
+    if logits.dim() < 1 or logits.shape[-1] < 1:
+        raise VerifyAttnError("logits need a vocabulary axis")
+    lead, V = logits.shape[:-1], logits.shape[-1]
+    R = lead.numel()
+    a = VaLogprobArgs()
+    if R:
+        try:
+            rows = logits.view(R, V)
+        except RuntimeError:
+            raise VerifyAttnError("logits rows are not evenly spaced") from None
+        if V > 1 and rows.stride(1) != 1:
+            raise VerifyAttnError("logits rows are not dense")
+        a.ld = rows.stride(0) if R > 1 else V
+        a.logits = logits.data_ptr()
+    else:
+        a.ld = V
+    a.dtype = VA_F32 if logits.dtype == torch.float32 else VA_BF16
+    a.R, a.V, a.K, a.scale = R, V, int(k), float(scale)
+    if not 0 <= a.K <= 16:
+        raise VerifyAttnError("k is not in 0 .. 16")
+    with _on(logits, stream):
+        f32 = dict(device=logits.device, dtype=torch.float32)
+        lse, entropy = torch.empty(lead, **f32), torch.empty(lead, **f32)
+        a.lse, a.entropy = lse.data_ptr(), entropy.data_ptr()
+        tok_lp = top_ids = top_lp = None
+        if tokens is not None:
+            G = 1 if tokens.shape == lead else tokens.shape[-1] if tokens.dim() else 0
+            want = lead if tokens.shape == lead else lead + (G,)
+            a.tokens, a.G = _need(tokens, "tokens", logits, (torch.int32,), want), G
+            tok_lp = torch.empty(tokens.shape, **f32)
+            a.tok_lp = tok_lp.data_ptr()
+        if a.K:
+            top_ids = torch.empty(lead + (a.K,), device=logits.device, dtype=torch.int32)
+            top_lp = torch.empty(lead + (a.K,), device=logits.device,
+                                 dtype=torch.float64 if wide else torch.float32)
+            a.top_ids = top_ids.data_ptr()
+            if wide:
+                a.top_lp64 = top_lp.data_ptr()
+            else:
+                a.top_lp = top_lp.data_ptr()
+        if row_status is not None:
+            a.row_status = _need(row_status, "row_status", logits, (torch.int32,), lead)
+        _check(load_library().va_token_logprobs(ctypes.byref(a), _stream()), "va_token_logprobs")
+    return TokenLogprobs(lse, entropy, tok_lp, top_ids, top_lp)
+
+
+def key_weights(q_nope, q_pe, c_kv, k_pe, page_table, kv_len, tree_mask, lse, *, scale: float,
+                path=None, accept_len=None, weights=None, decay: float = 1.0, out=None,
+                workspace=None, req_status=None, flags: int = 0, kv_scale: float = 1.0,
+                stream=None):
+    """Attention weight that each cached key received, accumulated: what evict_plan ranks by.
+
+    The first seven arguments and scale are verify_attn's, lse [B,T,H] is what it
+    returned.  With path [B,T] and accept_len [B] (tree_accept's) only the accepted
+    nodes count.  Returns out = decay * weights + the new sums, float32
+    [B, 64 * max_pages]; slots from kv_len on are not touched (zeros in an array
+    allocated here).  out may be weights."""
+    import torch
+    if q_nope.dim() != 4:
+        raise VerifyAttnError("q_nope is not [B, T, H, 512]")
+    B, T, H, _ = q_nope.shape
+    i32, f32 = (torch.int32,), (torch.float32,)
+    qd = (torch.float32, torch.bfloat16)
+    a = VaKeyWeightArgs()
+    a.q_nope = _need(q_nope, "q_nope", q_nope, qd, (B, T, H, D_LATENT))
+    a.q_pe = _need(q_pe, "q_pe", q_nope, (q_nope.dtype,), (B, T, H, D_ROPE))
+    fp8 = _fp8_cache(c_kv)
+    kd = (c_kv.dtype,) if fp8 else (q_nope.dtype,)
+    n = c_kv.shape[0]
+    a.c_kv = _need(c_kv, "c_kv", q_nope, kd, (n, PAGE_SIZE, D_LATENT))
+    a.k_pe = _need(k_pe, "k_pe", q_nope, kd, (n, PAGE_SIZE, D_ROPE))
+    m = page_table.shape[-1]
+    a.page_table = _need(page_table, "page_table", q_nope, i32, (B, m))
+    a.kv_len = _need(kv_len, "kv_len", q_nope, i32, (B,))
+    a.tree_mask = _need(tree_mask, "tree_mask", q_nope, (torch.int64,), (B, T, (T + 63) // 64))
+    a.lse = _need(lse, "lse", q_nope, f32, (B, T, H))
+    if path is not None:
+        a.path = _need(path, "path", q_nope, i32, (B, T))
+    if accept_len is not None:
+        a.accept_len = _need(accept_len, "accept_len", q_nope, i32, (B,))
+    cap = (B, m * PAGE_SIZE)
+    if weights is not None:
+        a.weights_in = _need(weights, "weights", q_nope, f32, cap)
+    if req_status is not None:
+        a.req_status = _need(req_status, "req_status", q_nope, i32, (B,))
+    a.dtype = VA_F32 if q_nope.dtype == torch.float32 else VA_BF16
+    a.B, a.H, a.T, a.scale, a.decay = B, H, T, float(scale), float(decay)
+    a.num_pages, a.page_size, a.max_pages = n, PAGE_SIZE, m
+    a.flags = flags | (VA_FLAG_KV_FP8_E4M3 if fp8 else 0)
+    a.kv_scale = float(kv_scale)
+    with _on(q_nope, stream):
+        if out is None:
+            out = torch.zeros(cap, device=q_nope.device, dtype=torch.float32)
+        a.weights = _need(out, "out", q_nope, f32, cap)
+        lib = load_library()
+        need = lib.va_key_weights_workspace_bytes(ctypes.byref(a))
+        if need and workspace is None:
+            workspace = torch.empty(need, device=q_nope.device, dtype=torch.uint8)
+        if workspace is not None:
+            a.workspace = workspace.data_ptr()
+            a.workspace_bytes = workspace.numel() * workspace.element_size()
+        _check(lib.va_key_weights(ctypes.byref(a), _stream()), "va_key_weights")
+    return out
+
+
+class EvictPlan(NamedTuple):
+    """What evict_plan returns."""
+
+    new_len: Any    # int32 [B]
+    from_slot: Any  # int32 [B, capacity], -1 from new_len on
+    weights: Any    # float32 [B, capacity]
+    pos: Any        # int32 [B, capacity], or None without positions
+
+
+def evict_plan(weights, kv_len, budget, *, path=None, accept_len=None, tree_len: int = 0, pos=None,
+               n_sink: int = 0, n_recent: int = 0, weights_out=None, pos_out=None,
+               req_status=None, stream=None) -> EvictPlan:
+    """Which cached keys stay, and in which slots (kv_move then moves a layer's keys).
+
+    weights float32 [B, capacity] (key_weights), kv_len and budget int32 [B].  With
+    tree_len = T the last T keys are the tree's nodes: path [B,T] and accept_len [B]
+    (tree_accept's) say which of them stay, and the others are dropped.  pos int32
+    [B, capacity] holds each slot's token position where an earlier eviction has
+    reordered them.  weights_out and pos_out may be weights and pos."""
+    import torch
+    if weights.dim() != 2:
+        raise VerifyAttnError("weights are not [B, capacity]")
+    i32, f32 = (torch.int32,), (torch.float32,)
+    B, cap = weights.shape
+    a = VaEvictArgs()
+    a.B, a.capacity, a.T, a.n_sink, a.n_recent = B, cap, tree_len, n_sink, n_recent
+    a.weights = _need(weights, "weights", weights, f32, (B, cap))
+    a.kv_len = _need(kv_len, "kv_len", weights, i32, (B,))
+    a.budget = _need(budget, "budget", weights, i32, (B,))
+    if path is not None:
+        a.path = _need(path, "path", weights, i32, (B, tree_len))
+    if accept_len is not None:
+        a.accept_len = _need(accept_len, "accept_len", weights, i32, (B,))
+    if pos is not None:
+        a.pos = _need(pos, "pos", weights, i32, (B, cap))
+    elif pos_out is not None:
+        raise VerifyAttnError("pos_out without pos")
+    if req_status is not None:
+        a.req_status = _need(req_status, "req_status", weights, i32, (B,))
+    with _on(weights, stream):
+        new_len, from_slot = torch.empty_like(kv_len), torch.empty(B, cap, device=weights.device,
+                                                                   dtype=torch.int32)
+        a.new_len, a.from_slot = new_len.data_ptr(), from_slot.data_ptr()
+        if weights_out is None:
+            weights_out = torch.empty_like(weights)
+        a.weights_out = _need(weights_out, "weights_out", weights, f32, (B, cap))
+        if pos is not None:
+            if pos_out is None:
+                pos_out = torch.empty_like(pos)
+            a.pos_out = _need(pos_out, "pos_out", weights, i32, (B, cap))
+        _check(load_library().va_evict_plan(ctypes.byref(a), _stream()), "va_evict_plan")
+    return EvictPlan(new_len, from_slot, weights_out, pos_out)
+
+
+def kv_move(c_kv, k_pe, page_table, from_slot, new_len, *, req_status=None, stream=None) -> None:
+    """Moves the keys of one cache, in place, as an evict_plan says.
+
+    c_kv [pages,64,512] and k_pe [pages,64,64] of any cache type (float32, bfloat16 or
+    8-bit codes); from_slot and new_len are the plan's.  Every page up to a request's
+    old length must be that request's alone."""
+    import torch
+    i32 = (torch.int32,)
+    n, (B, m) = c_kv.shape[0], page_table.shape
+    kinds = (torch.float32, torch.bfloat16, torch.uint8, torch.float8_e4m3fn)
+    if B == 0:
+        return
+    c = _need(c_kv, "c_kv", c_kv, kinds, (n, PAGE_SIZE, D_LATENT))
+    k = _need(k_pe, "k_pe", c_kv, (c_kv.dtype,), (n, PAGE_SIZE, D_ROPE))
+    t = _need(page_table, "page_table", c_kv, i32, (B, m))
+    f = _need(from_slot, "from_slot", c_kv, i32, (B, m * PAGE_SIZE))
+    l = _need(new_len, "new_len", c_kv, i32, (B,))
+    s = None if req_status is None else _need(req_status, "req_status", c_kv, i32, (B,))
+    with _on(c_kv, stream):
+        _check(load_library().va_kv_move(c, k, c_kv.element_size(), n, PAGE_SIZE, t, B, m, f, l, s,
+                                         _stream()), "va_kv_move")

@@ -3,9 +3,11 @@
 // launching anything; the caller owns all device memory.
 #include <atomic>
 #include <cfloat>
+#include <cmath>
 #include <cstdio>
 
 #include "va_common.cuh"
+#include "va_kweights.cuh"
 
 namespace {
 
@@ -101,6 +103,56 @@ int plan_splits(const va_attn_args* a) {
     if (units * 10 >= waves * slots * 9) return S;
   }
   return VA_MAX_SPLITS;
+}
+
+int check_key_weights(const va_key_weight_args* a) {
+  if (!a) return VA_ERR_INVALID_ARG;
+  if (a->dtype != VA_F32 && a->dtype != VA_BF16) return VA_ERR_INVALID_ARG;
+  if (a->B < 0 || a->H < 1 || a->T < 1 || a->T > VA_MAX_QLEN) return VA_ERR_INVALID_ARG;
+  if (a->page_size != VA_PAGE_SIZE || a->B > VA_MAX_BATCH) return VA_ERR_UNSUPPORTED;
+  if (a->flags & ~(VA_FLAG_BF16_CUDA_CORES | VA_FLAG_KV_FP8_E4M3)) return VA_ERR_INVALID_ARG;
+  if ((a->flags & VA_FLAG_KV_FP8_E4M3) && !(a->kv_scale > 0.f && a->kv_scale <= FLT_MAX))
+    return VA_ERR_INVALID_ARG;
+  if (!(fabsf(a->scale) <= FLT_MAX) || !(fabsf(a->decay) <= FLT_MAX)) return VA_ERR_INVALID_ARG;
+  if (a->B == 0) return VA_OK;
+  if (a->num_pages < 1 || a->max_pages < 1) return VA_ERR_INVALID_ARG;
+  if ((long long)a->num_pages * VA_PAGE_SIZE > 0x7fffffffLL ||
+      (long long)a->max_pages * VA_PAGE_SIZE > 0x7fffffffLL - VA_SPLIT_ALIGN ||
+      (long long)a->B * a->T * a->H > 0x7fffffffLL)
+    return VA_ERR_UNSUPPORTED;  // pool rows, slots and query rows are 32-bit
+  for (const void* p : {a->q_nope, a->q_pe, a->c_kv, a->k_pe})
+    if (!p || !aligned(p, 16)) return VA_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)a->page_table, (const void*)a->kv_len, (const void*)a->lse,
+                        (const void*)a->weights})
+    if (!p || !aligned(p, 4)) return VA_ERR_INVALID_ARG;
+  if (!a->tree_mask || !aligned(a->tree_mask, 8)) return VA_ERR_INVALID_ARG;
+  if ((a->path == nullptr) != (a->accept_len == nullptr)) return VA_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)a->path, (const void*)a->accept_len,
+                        (const void*)a->weights_in, (const void*)a->req_status})
+    if (p && !aligned(p, 4)) return VA_ERR_INVALID_ARG;
+  return VA_OK;
+}
+
+// Row splits of a key-weight call (grid z).  A CTA's work is its key tile
+// times its share of the row blocks; rows are split while the key tiles alone
+// would leave SMs idle.  With an accepted path the host does not know its
+// length: a path of the deepest tree is assumed, and splits without rows only
+// write zeros.
+int key_weight_splits(const va_key_weight_args* a) {
+  const int sms = sm_count();
+  const int nodes = a->path && a->T > VA_MAX_DEPTH + 1 ? VA_MAX_DEPTH + 1 : a->T;
+  const long long blocks = ((long long)nodes * a->H + va::kKwRows - 1) / va::kKwRows;
+  const long long tiles =
+      (long long)a->B * (((long long)a->max_pages * VA_PAGE_SIZE + va::kKwKeys - 1) / va::kKwKeys);
+  long long s = (2LL * sms + tiles - 1) / tiles;
+  if (s > blocks) s = blocks;
+  if (s > VA_MAX_SPLITS) s = VA_MAX_SPLITS;
+  return s < 1 ? 1 : (int)s;
+}
+
+size_t key_weight_workspace(const va_key_weight_args* a, int splits) {
+  if (splits < 2) return 0;
+  return va::align256((size_t)splits * a->B * a->max_pages * VA_PAGE_SIZE * sizeof(float));
 }
 
 }  // namespace
@@ -285,6 +337,111 @@ int va_merge(const float* o_part, const float* lse_part, int S, int B, int T, in
     return VA_ERR_INVALID_ARG;
   cudaError_t e = va::launch_merge(o_part, lse_part, S, (long long)B * T * H, out_dtype, out,
                                    lse, (cudaStream_t)stream);
+  return e == cudaSuccess ? VA_OK : VA_ERR_CUDA;
+}
+
+int va_token_logprobs(const va_logprob_args* a, va_stream_t stream) {
+  if (!a) return VA_ERR_INVALID_ARG;
+  if (a->dtype != VA_F32 && a->dtype != VA_BF16) return VA_ERR_INVALID_ARG;
+  if (a->R < 0 || a->V < 1 || a->ld < a->V || a->G < 0 || a->G > 65536 || a->K < 0 ||
+      a->K > VA_MAX_TOPK || a->K > a->V)
+    return VA_ERR_INVALID_ARG;
+  if (!(a->scale > 0.f && a->scale <= FLT_MAX)) return VA_ERR_INVALID_ARG;
+  if (a->R == 0) return VA_OK;
+  if (a->R > 0x7fffffff / 8 || a->V > 0x7fffffff - 65536) return VA_ERR_UNSUPPORTED;
+  if (!a->logits || !aligned(a->logits, a->dtype == VA_F32 ? 4 : 2)) return VA_ERR_INVALID_ARG;
+  if (a->G > 0 && (!a->tokens || !a->tok_lp)) return VA_ERR_INVALID_ARG;
+  if (a->K > 0 && !a->top_ids) return VA_ERR_INVALID_ARG;
+  if (a->K == 0 && (a->top_lp || a->top_lp64)) return VA_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)a->tokens, (const void*)a->lse, (const void*)a->entropy,
+                        (const void*)a->tok_lp, (const void*)a->top_ids, (const void*)a->top_lp,
+                        (const void*)a->row_status})
+    if (p && !aligned(p, 4)) return VA_ERR_INVALID_ARG;
+  if (a->top_lp64 && !aligned(a->top_lp64, 8)) return VA_ERR_INVALID_ARG;
+  cudaError_t e = va::launch_logprobs(*a, sm_count(), (cudaStream_t)stream);
+  return e == cudaSuccess ? VA_OK : VA_ERR_CUDA;
+}
+
+size_t va_key_weights_workspace_bytes(const va_key_weight_args* args) {
+  if (check_key_weights(args) != VA_OK || args->B == 0) return 0;
+  return key_weight_workspace(args, key_weight_splits(args));
+}
+
+int va_key_weights(const va_key_weight_args* args, va_stream_t stream) {
+  const int st = check_key_weights(args);
+  if (st != VA_OK) return st;
+  if (args->B == 0) return VA_OK;
+  const int splits = key_weight_splits(args);
+  const size_t need = key_weight_workspace(args, splits);
+  if (need && (!args->workspace || !aligned(args->workspace, 256) || args->workspace_bytes < need))
+    return VA_ERR_INVALID_ARG;
+  va::KwParams p;
+  p.q_nope = args->q_nope;
+  p.q_pe = args->q_pe;
+  p.c_kv = args->c_kv;
+  p.k_pe = args->k_pe;
+  p.page_table = args->page_table;
+  p.kv_len = args->kv_len;
+  p.tree_mask = args->tree_mask;
+  p.lse = args->lse;
+  p.path = args->path;
+  p.accept_len = args->accept_len;
+  p.weights_in = args->weights_in;
+  p.weights = args->weights;
+  p.part = need ? static_cast<float*>(args->workspace) : nullptr;
+  p.req_status = args->req_status;
+  p.B = args->B;
+  p.H = args->H;
+  p.T = args->T;
+  p.max_pages = args->max_pages;
+  p.num_pages = args->num_pages;
+  p.splits = splits;
+  p.scale = (args->flags & VA_FLAG_KV_FP8_E4M3) ? args->scale * args->kv_scale : args->scale;
+  p.decay = args->decay;
+  cudaError_t e = va::launch_kweights_simt(*args, p, (cudaStream_t)stream);
+  if (e == cudaSuccess && splits > 1) e = va::launch_kweights_join(p, (cudaStream_t)stream);
+  return e == cudaSuccess ? VA_OK : VA_ERR_CUDA;
+}
+
+int va_evict_plan(const va_evict_args* a, va_stream_t stream) {
+  if (!a) return VA_ERR_INVALID_ARG;
+  if (a->B < 0 || a->T < 0 || a->T > VA_MAX_QLEN || a->n_sink < 0 || a->n_recent < 0)
+    return VA_ERR_INVALID_ARG;
+  if (a->B == 0) return VA_OK;
+  if (a->capacity < 1 || a->capacity < a->T) return VA_ERR_INVALID_ARG;
+  if (a->B > VA_MAX_BATCH) return VA_ERR_UNSUPPORTED;
+  for (const void* p : {(const void*)a->weights, (const void*)a->kv_len, (const void*)a->budget,
+                        (const void*)a->new_len, (const void*)a->from_slot})
+    if (!p || !aligned(p, 4)) return VA_ERR_INVALID_ARG;
+  if ((a->T > 0) != (a->path != nullptr) || (a->T > 0) != (a->accept_len != nullptr))
+    return VA_ERR_INVALID_ARG;
+  if (a->pos_out && !a->pos) return VA_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)a->path, (const void*)a->accept_len, (const void*)a->pos,
+                        (const void*)a->weights_out, (const void*)a->pos_out,
+                        (const void*)a->req_status})
+    if (p && !aligned(p, 4)) return VA_ERR_INVALID_ARG;
+  cudaError_t e = va::launch_evict_plan(*a, sm_count(), (cudaStream_t)stream);
+  if (e == cudaErrorNotSupported) return VA_ERR_UNSUPPORTED;
+  return e == cudaSuccess ? VA_OK : VA_ERR_CUDA;
+}
+
+int va_kv_move(void* c_kv, void* k_pe, int elem_bytes, int num_pages, int page_size,
+               const int32_t* page_table, int B, int max_pages, const int32_t* from_slot,
+               const int32_t* new_len, int32_t* req_status, va_stream_t stream) {
+  if (B < 0 || (elem_bytes != 1 && elem_bytes != 2 && elem_bytes != 4)) return VA_ERR_INVALID_ARG;
+  if (page_size != VA_PAGE_SIZE || B > VA_MAX_BATCH) return VA_ERR_UNSUPPORTED;
+  if (B == 0) return VA_OK;
+  if (num_pages < 1 || max_pages < 1) return VA_ERR_INVALID_ARG;
+  if ((long long)num_pages * VA_PAGE_SIZE > 0x7fffffffLL ||
+      (long long)max_pages * VA_PAGE_SIZE > 0x7fffffffLL)
+    return VA_ERR_UNSUPPORTED;
+  for (const void* p : {(const void*)c_kv, (const void*)k_pe})
+    if (!p || !aligned(p, 16)) return VA_ERR_INVALID_ARG;
+  for (const void* p : {(const void*)page_table, (const void*)from_slot, (const void*)new_len})
+    if (!p || !aligned(p, 4)) return VA_ERR_INVALID_ARG;
+  if (req_status && !aligned(req_status, 4)) return VA_ERR_INVALID_ARG;
+  cudaError_t e = va::launch_kv_move(c_kv, k_pe, elem_bytes, num_pages, page_table, B, max_pages,
+                                     from_slot, new_len, req_status, (cudaStream_t)stream);
   return e == cudaSuccess ? VA_OK : VA_ERR_CUDA;
 }
 

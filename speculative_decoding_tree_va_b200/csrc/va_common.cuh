@@ -185,6 +185,15 @@ cudaError_t launch_attn_tc(const va_attn_args& a, SplitRange sp, const int32_t* 
 cudaError_t launch_kv_widen(const va_attn_args& a, void* w_ckv, void* w_kpe, int32_t* w_table,
                             cudaStream_t st);
 
+// Around the verify call (va_logprobs.cu, va_evict.cu); `sms` is the device's
+// SM count, which the launch shapes are planned for.
+cudaError_t launch_logprobs(const va_logprob_args& a, int sms, cudaStream_t st);
+cudaError_t launch_evict_plan(const va_evict_args& a, int sms, cudaStream_t st);
+cudaError_t launch_kv_move(void* c_kv, void* k_pe, int elem_bytes, int num_pages,
+                           const int32_t* page_table, int B, int max_pages,
+                           const int32_t* from_slot, const int32_t* new_len, int32_t* req_status,
+                           cudaStream_t st);
+
 // Everything va_verify_attn launches once its arguments are checked and its
 // split count S is known, with the workspace at `ws` laid out as above.
 int run_verify(const va_attn_args& a, int S, void* ws, cudaStream_t st);

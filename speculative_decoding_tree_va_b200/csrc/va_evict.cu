@@ -1,0 +1,493 @@
+// Eviction from the paged latent cache by accumulated attention weight: the
+// plan (which keys stay, in which slots) and the move of one cache's keys.
+//
+// Plan.  One cluster per request; CTA r of C owns a contiguous part of the
+// slots.  The k heaviest unprotected candidates are found by a radix select
+// on order-preserving bits of the weights (digits of 11, 11 and 10 bits; one
+// shared-memory histogram per CTA, joined over distributed shared memory),
+// ties by lower slot through each CTA's count of the last digit.  Kept slots
+// at or above the new length ("movers") fill the free slots below it
+// ("holes"), both in ascending order: two block scans per tile give their
+// indices, the holes are listed in the still unused end of from_slot, and
+// each mover looks its hole up.  Order-preserving compaction would move
+// every key behind the first hole; this moves only those past the new length.
+//
+// Move.  A CTA per 64 destination slots lists the slots that change and
+// copies their rows with 16-byte accesses.  No slot is both source and
+// destination, so the copy is in place and in any order.
+//
+// Both are bound by memory: 8 bytes a slot and an array for the plan, two
+// row accesses per moved key for the move.
+#include <climits>
+
+#include "va_common.cuh"
+
+namespace va {
+namespace {
+
+constexpr int kNT = 1024;
+constexpr int kVec = 4;               // consecutive slots of a thread in a tile
+constexpr int kTile = kNT * kVec;
+constexpr int kBins = 2048;
+constexpr int kMaxKeepBytes = 128 * 1024;  // keep bits of a CTA's slots in shared memory
+constexpr int kMaxCluster = 8;
+constexpr unsigned kFull = 0xffffffffu;
+
+struct PlanParams {
+  const float* weights;
+  const int32_t* kv_len;
+  const int32_t* budget;
+  const int32_t* path;
+  const int32_t* accept_len;
+  const int32_t* pos;
+  int cap, T, n_sink, n_recent;
+  int32_t* new_len;
+  int32_t* from_slot;
+  float* weights_out;
+  int32_t* pos_out;
+  int32_t* req_status;
+};
+
+// Slots of each CTA of a cluster of C, a whole number of threads' quads.
+__host__ __device__ __forceinline__ int slots_per_cta(int cap, int C) {
+  return (int)(((long long)cap + C - 1) / C + kVec - 1) / kVec * kVec;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t remote_u32(const void* p, uint32_t rank) {
+  uint32_t a, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+// Bits that order like the weight: -0 like +0, NaN like -inf.
+__device__ __forceinline__ uint32_t order_bits(float x) {
+  if (!(x == x)) x = -INFINITY;
+  const uint32_t u = __float_as_uint(x + 0.0f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+struct Shared {
+  uint32_t hist[2][kBins];
+  uint32_t warp_sum[32];
+  uint32_t total;
+  int32_t newest;                 // of this CTA
+  uint32_t cnt[4];                // protected | ties | kept below new_len | kept from it on
+  uint32_t pick[3];               // digit, keys above it, keys in it
+  uint32_t acc[3];                // accepted nodes, one bit each
+  int bad;
+};
+
+// Exclusive prefix sum over the CTA's threads; the total goes to *total.
+__device__ uint32_t block_scan(uint32_t v, Shared& s, uint32_t* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t x = v;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const uint32_t y = __shfl_up_sync(kFull, x, d);
+    if (lane >= d) x += y;
+  }
+  if (lane == 31) s.warp_sum[warp] = x;
+  __syncthreads();
+  if (warp == 0) {
+    uint32_t w = s.warp_sum[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t y = __shfl_up_sync(kFull, w, d);
+      if (lane >= d) w += y;
+    }
+    s.warp_sum[lane] = w;  // inclusive over warps
+  }
+  __syncthreads();
+  const uint32_t before = (warp ? s.warp_sum[warp - 1] : 0) + x - v;
+  *total = s.warp_sum[31];
+  __syncthreads();
+  return before;
+}
+
+__global__ void __launch_bounds__(kNT) evict_plan_kernel(const PlanParams p, int C) {
+  __shared__ Shared s;
+  extern __shared__ uint8_t keep4[];  // keep bits of this CTA's slots, one quad a byte
+  const int tid = threadIdx.x, lane = tid & 31;
+  const uint32_t rank = C > 1 ? cluster_rank() : 0;
+  const int b = blockIdx.x / C;
+  const size_t row = (size_t)b * p.cap;
+  const float* w = p.weights + row;
+  const int32_t* pos = p.pos ? p.pos + row : nullptr;
+  const int T = p.T, cap = p.cap;
+  const int len = p.kv_len[b];
+  auto sync = [&]() {
+    if (C > 1)
+      asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;"
+                   ::: "memory");
+    else
+      __syncthreads();
+  };
+
+  // request checks: kv_len, then the accepted path (ascending nodes)
+  const bool len_ok = len >= T && len <= cap;
+  const int n_acc_in = T > 0 ? p.accept_len[b] : 0;
+  if (tid == 0) { s.bad = 0; s.newest = -1; }
+  if (tid < 3) s.acc[tid] = 0;
+  if (tid < 4) s.cnt[tid] = 0;
+  for (int i = tid; i < 2 * kBins; i += kNT) (&s.hist[0][0])[i] = 0;
+  __syncthreads();
+  bool path_ok = n_acc_in >= 0 && n_acc_in <= T;
+  if (path_ok && tid < n_acc_in) {
+    const int n = p.path[(size_t)b * T + tid];
+    const int prev = tid ? p.path[(size_t)b * T + tid - 1] : -1;
+    if (n <= prev || n >= T || prev < -1) s.bad = 1;
+    else atomicOr(&s.acc[n >> 5], 1u << (n & 31));
+  }
+  __syncthreads();
+  path_ok = path_ok && !s.bad;
+  if ((!len_ok || !path_ok) && rank == 0 && tid == 0 && p.req_status)
+    p.req_status[b] = VA_ERR_INVALID_ARG;
+  const int N = len_ok ? len : 0;       // slots in use
+  const int P = len_ok ? len - T : 0;   // prefix
+  const bool asis = len_ok && !path_ok;
+  const uint32_t a0 = s.acc[0], a1 = s.acc[1], a2 = s.acc[2];
+  const int n_acc = N > 0 && !asis ? n_acc_in : 0;
+
+  // this CTA's slots, in whole quads
+  const int per = slots_per_cta(cap, C);
+  const int lo = min(cap, (int)rank * per), hi = min(cap, lo + per);
+  const int hiN = min(hi, max(lo, N));
+
+  auto accepted = [&](int j) {
+    const int n = j - P;
+    return n >= 0 && n < T && (((n < 32 ? a0 : n < 64 ? a1 : a2) >> (n & 31)) & 1u);
+  };
+
+  // newest position of a candidate
+  int newest = 0;
+  if (p.n_recent > 0) {
+    if (!pos) {
+      int last = P - 1;
+      for (int n = 0; n < T; ++n)
+        if (accepted(P + n)) last = P + n;
+      newest = last;
+    } else {
+      int mine = INT_MIN;
+      for (int j = lo + tid; j < hiN; j += kNT)
+        if (j < P || accepted(j)) mine = max(mine, pos[j]);
+      if (tid == 0) s.newest = INT_MIN;
+      __syncthreads();
+      mine = __reduce_max_sync(kFull, mine);
+      if (lane == 0) atomicMax(&s.newest, mine);
+      sync();
+      newest = s.newest;
+      if (C > 1)
+        for (int r = 0; r < C; ++r) newest = max(newest, (int)remote_u32(&s.newest, r));
+    }
+  }
+  // class of a slot: 0 dropped, 1 ranked by weight, 2 protected
+  auto group = [&](int j) {
+    if (j >= P) return accepted(j) ? 2 : 0;
+    const int q = pos ? pos[j] : j;
+    if (q < p.n_sink || (p.n_recent > 0 && (long long)newest - q < p.n_recent)) return 2;
+    return 1;
+  };
+
+  // protected keys, and the first digit's histogram
+  {
+    uint32_t prot = 0;
+    for (int j = lo + tid; j < hiN; j += kNT) {
+      const int g = group(j);
+      prot += g == 2;
+      if (g == 1) atomicAdd(&s.hist[0][order_bits(w[j]) >> 21], 1u);
+    }
+    prot = __reduce_add_sync(kFull, prot);
+    if (lane == 0 && prot) atomicAdd(&s.cnt[0], prot);
+  }
+  sync();
+  uint32_t n_prot = s.cnt[0];
+  if (C > 1) {
+    n_prot = 0;
+    for (int r = 0; r < C; ++r) n_prot += remote_u32(&s.cnt[0], r);
+  }
+  const int n_cand = P + n_acc;
+  const int n_other = n_cand - (int)n_prot;
+  const int n_new = asis ? N : max(min(max(p.budget[b], 0), n_cand), (int)n_prot);
+  const int k = n_new - (int)n_prot;  // how many of the others stay
+  const bool select = !asis && k > 0 && k < n_other;
+
+  // radix select: the k-th largest key of the others, and how many equal to
+  // it stay.  Keys above `key_lo` stay; `ties` of those equal to it.
+  uint32_t prefix = 0, need = (uint32_t)max(k, 0), ties_before = 0;
+  if (select) {
+    for (int pass = 0; pass < 3; ++pass) {
+      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+      const int bins = pass == 2 ? 1024 : 2048;
+      uint32_t* h = s.hist[pass & 1];
+      if (pass > 0) {
+        const int above = pass == 1 ? 21 : 10;
+        for (int j = lo + tid; j < hiN; j += kNT) {
+          if (group(j) != 1) continue;
+          const uint32_t o = order_bits(w[j]);
+          if ((o >> above) == (prefix >> above)) atomicAdd(&h[(o >> shift) & (bins - 1)], 1u);
+        }
+        sync();
+      }
+      // thread t holds the two highest remaining bins in descending order
+      uint32_t c0 = 0, c1 = 0;
+      const int d0 = bins - 1 - 2 * tid;
+      if (d0 > 0) {
+        if (C > 1) {
+          for (int r = 0; r < C; ++r) {
+            c0 += remote_u32(&h[d0], r);
+            c1 += remote_u32(&h[d0 - 1], r);
+          }
+        } else {
+          c0 = h[d0];
+          c1 = h[d0 - 1];
+        }
+      }
+      uint32_t total;
+      const uint32_t before = block_scan(c0 + c1, s, &total);
+      if (d0 > 0 && before < need && need <= before + c0 + c1) {
+        const bool second = need > before + c0;
+        s.pick[0] = (uint32_t)(second ? d0 - 1 : d0);
+        s.pick[1] = before + (second ? c0 : 0);
+      }
+      // the other buffer is read by no one any more: clear it for the next pass
+      if (pass > 0)
+        for (int i = tid; i < kBins; i += kNT) s.hist[(pass + 1) & 1][i] = 0;
+      __syncthreads();
+      prefix |= s.pick[0] << shift;
+      need -= s.pick[1];
+      if (pass == 2) {
+        const uint32_t digit = prefix & 1023u;
+        for (int r = 0; r < (int)rank; ++r) ties_before += remote_u32(&h[digit], r);
+      }
+      __syncthreads();
+    }
+  }
+  const uint32_t key_lo = prefix;
+
+  // One tile: which of this thread's slots stay.  `tie` counts the ties seen
+  // in earlier tiles (same value in every thread).
+  auto keep_bits = [&](int t0, uint32_t& tie) {
+    const int j0 = t0 + tid * kVec;
+    uint32_t keep = 0, eq = 0;
+#pragma unroll
+    for (int i = 0; i < kVec; ++i) {
+      const int j = j0 + i;
+      if (j >= hiN) continue;
+      if (asis) { keep |= 1u << i; continue; }
+      const int g = group(j);
+      if (g == 2) keep |= 1u << i;
+      if (g == 1 && k > 0) {
+        if (!select) keep |= 1u << i;
+        else {
+          const uint32_t o = order_bits(w[j]);
+          if (o > key_lo) keep |= 1u << i;
+          if (o == key_lo) eq |= 1u << i;
+        }
+      }
+    }
+    if (select) {
+      uint32_t total;
+      uint32_t at = tie + block_scan(__popc(eq), s, &total);
+      tie += total;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i)
+        if (eq >> i & 1u) {
+          if (at < need) keep |= 1u << i;
+          ++at;
+        }
+    }
+    return keep;
+  };
+  // slots of this thread's quad that lie below n_new
+  auto below_bits = [&](int j0) {
+    const int n = min(max(n_new - j0, 0), kVec);
+    return (1u << n) - 1u;
+  };
+  auto in_bits = [&](int j0) {
+    const int n = min(max(hi - j0, 0), kVec);
+    return (1u << n) - 1u;
+  };
+
+  // holes and movers of this CTA, counted, then joined over the cluster.  The
+  // keep bits are held from here on: the outputs may overwrite the inputs.
+  {
+    uint32_t tie = ties_before, holes = 0, movers = 0;
+    for (int t0 = lo; t0 < hi; t0 += kTile) {
+      const uint32_t keep = keep_bits(t0, tie);
+      const int j0 = t0 + tid * kVec;
+      if (j0 < hi) keep4[(j0 - lo) / kVec] = (uint8_t)keep;
+      holes += __popc(~keep & below_bits(j0) & in_bits(j0));
+      movers += __popc(keep & ~below_bits(j0));
+    }
+    holes = __reduce_add_sync(kFull, holes);
+    movers = __reduce_add_sync(kFull, movers);
+    if (lane == 0 && holes) atomicAdd(&s.cnt[2], holes);
+    if (lane == 0 && movers) atomicAdd(&s.cnt[3], movers);
+  }
+  sync();
+  uint32_t hole_at = 0, mover_at = 0;
+  for (int r = 0; r < (int)rank; ++r) {
+    hole_at += remote_u32(&s.cnt[2], r);
+    mover_at += remote_u32(&s.cnt[3], r);
+  }
+  // list the holes in from_slot[n_new ..): there are as many as movers, which
+  // all lie there, so the list fits
+  {
+    uint32_t at = hole_at;
+    for (int t0 = lo; t0 < min(hi, n_new); t0 += kTile) {
+      const int j0 = t0 + tid * kVec;
+      const uint32_t keep = j0 < hi ? keep4[(j0 - lo) / kVec] : 0;
+      const uint32_t hole = ~keep & below_bits(j0) & in_bits(j0);
+      uint32_t total;
+      uint32_t i = at + block_scan(__popc(hole), s, &total);
+      at += total;
+#pragma unroll
+      for (int v = 0; v < kVec; ++v)
+        if (hole >> v & 1u) p.from_slot[row + n_new + i++] = j0 + v;
+    }
+  }
+  __threadfence();
+  sync();
+  // kept slots below n_new keep their key; a mover's key goes to its hole
+  {
+    uint32_t at = mover_at;
+    for (int t0 = lo; t0 < hiN; t0 += kTile) {
+      const int j0 = t0 + tid * kVec;
+      const uint32_t keep = j0 < hi ? keep4[(j0 - lo) / kVec] : 0;
+      const uint32_t mover = keep & ~below_bits(j0);
+      uint32_t total;
+      uint32_t i = at + block_scan(__popc(mover), s, &total);
+      at += total;
+#pragma unroll
+      for (int v = 0; v < kVec; ++v) {
+        if (!(keep >> v & 1u)) continue;
+        const int j = j0 + v;
+        int to = j;
+        if (mover >> v & 1u) to = __ldcg(&p.from_slot[row + n_new + i++]);
+        p.from_slot[row + to] = j;
+        if (p.weights_out) p.weights_out[row + to] = w[j];
+        if (p.pos_out) p.pos_out[row + to] = pos[j];
+      }
+    }
+  }
+  sync();
+  for (int j = max(lo, n_new) + tid; j < hi; j += kNT) {
+    p.from_slot[row + j] = -1;
+    if (p.weights_out) p.weights_out[row + j] = 0.f;
+    if (p.pos_out) p.pos_out[row + j] = -1;
+  }
+  if (rank == 0 && tid == 0) p.new_len[b] = n_new;
+}
+
+// ------------------------------------------------------------------- the move
+
+constexpr int kMoveThreads = 256;
+
+__global__ void __launch_bounds__(kMoveThreads)
+kv_move_kernel(uint4* __restrict__ c_kv, uint4* __restrict__ k_pe, int cw, int kw, int num_pages,
+               const int32_t* __restrict__ table, int max_pages,
+               const int32_t* __restrict__ from_slot, const int32_t* __restrict__ new_len,
+               int32_t* __restrict__ req_status) {
+  __shared__ int2 move[kPage];  // pool rows: destination, source
+  __shared__ int n_moves;
+  const int b = blockIdx.y, page = blockIdx.x, tid = threadIdx.x;
+  const int cap = max_pages * kPage;
+  const int n = new_len[b];
+  if (n < 0 || n > cap) {
+    if (page == 0 && tid == 0 && req_status) req_status[b] = VA_ERR_INVALID_ARG;
+    return;
+  }
+  if (page * kPage >= n) return;
+  if (tid == 0) n_moves = 0;
+  __syncthreads();
+  if (tid < kPage) {
+    const int d = page * kPage + tid;
+    const int f = d < n ? from_slot[(size_t)b * cap + d] : d;
+    if (f != d) {
+      const int32_t* t = table + (size_t)b * max_pages;
+      const int pd = t[page];
+      const int ps = f >= n && f < cap ? t[f / kPage] : -1;
+      if (pd < 0 || pd >= num_pages || ps < 0 || ps >= num_pages) {
+        if (req_status) req_status[b] = VA_ERR_INVALID_ARG;
+      } else {
+        move[atomicAdd(&n_moves, 1)] =
+            make_int2(pd * kPage + tid, ps * kPage + f % kPage);
+      }
+    }
+  }
+  __syncthreads();
+  const int per = cw + kw, total = n_moves * per;
+  for (int i = tid; i < total; i += kMoveThreads) {
+    const int2 m = move[i / per];
+    const int x = i % per;
+    if (x < cw) c_kv[(size_t)m.x * cw + x] = c_kv[(size_t)m.y * cw + x];
+    else k_pe[(size_t)m.x * kw + x - cw] = k_pe[(size_t)m.y * kw + x - cw];
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_evict_plan(const va_evict_args& a, int sms, cudaStream_t st) {
+  PlanParams p;
+  p.weights = a.weights;
+  p.kv_len = a.kv_len;
+  p.budget = a.budget;
+  p.path = a.path;
+  p.accept_len = a.accept_len;
+  p.pos = a.pos;
+  p.cap = a.capacity;
+  p.T = a.T;
+  p.n_sink = a.n_sink;
+  p.n_recent = a.n_recent;
+  p.new_len = a.new_len;
+  p.from_slot = a.from_slot;
+  p.weights_out = a.weights_out;
+  p.pos_out = a.pos ? a.pos_out : nullptr;
+  p.req_status = a.req_status;
+  // A request is cut over a cluster while its CTAs keep more than a tile each
+  // and the SMs are not yet covered, or their keep bits would not fit.
+  int C = 1;
+  while (C < kMaxCluster &&
+         (((long long)a.B * C < sms && (long long)a.capacity > (long long)kTile * C) ||
+          slots_per_cta(a.capacity, C) / kVec > kMaxKeepBytes))
+    C *= 2;
+  const int keep_bytes = slots_per_cta(a.capacity, C) / kVec;
+  if (keep_bytes > kMaxKeepBytes) return cudaErrorNotSupported;
+  if (keep_bytes > 24 * 1024) {  // past the default limit; the same value from every thread
+    cudaError_t e = cudaFuncSetAttribute(
+        evict_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKeepBytes);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = C;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((long long)a.B * C));
+  cfg.blockDim = dim3(kNT);
+  cfg.dynamicSmemBytes = keep_bytes;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = C > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, evict_plan_kernel, p, C);
+}
+
+cudaError_t launch_kv_move(void* c_kv, void* k_pe, int elem_bytes, int num_pages,
+                           const int32_t* page_table, int B, int max_pages,
+                           const int32_t* from_slot, const int32_t* new_len, int32_t* req_status,
+                           cudaStream_t st) {
+  const dim3 grid((unsigned)max_pages, (unsigned)B);
+  kv_move_kernel<<<grid, kMoveThreads, 0, st>>>(
+      static_cast<uint4*>(c_kv), static_cast<uint4*>(k_pe), kDc * elem_bytes / 16,
+      kDr * elem_bytes / 16, num_pages, page_table, max_pages, from_slot, new_len, req_status);
+  return cudaGetLastError();
+}
+
+}  // namespace va

@@ -1,0 +1,207 @@
+// Key weights on CUDA cores (fp32 queries, or bf16 on request), and the join
+// of row splits that the tensor-core kernel shares.
+//
+//   w_j = sum over counted rows r, j visible to r, of
+//         exp(scale q_r . k_j - lse_r)
+// With the log-sum-exp known the softmax needs no second statistic: one
+// product tile [128 keys x 128 rows] over the 576 dims, then the exponentials,
+// then a sum over the tile's rows that stays in the registers that hold its
+// keys.  The rows of a request are counted rows only: row r is head r % H of
+// the (r / H)-th accepted node.
+//
+// A CTA owns 128 keys and, when few key tiles would leave SMs idle, a share
+// of the row blocks (split); splits write partial sums that the join adds in
+// split order.  Bound by the FFMA rate: 576 multiply-adds per row and key.
+#include "va_common.cuh"
+#include "va_kweights.cuh"
+
+namespace va {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBK = 16;              // dims per step
+constexpr int kPitch = kKwKeys + 4;  // shared row of one dim
+
+__device__ __forceinline__ float ex2f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 8 consecutive elements at p (16-byte aligned for fp32, else to 8 elements).
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p);
+  const float4 b = *reinterpret_cast<const float4*>(p + 4);
+  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+  x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&x)[8]) {
+  const uint4 v = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8(const __nv_fp8_e4m3* p, float (&x)[8]) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  const uint32_t w[2] = {v.x, v.y};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_fp8x2_storage_t c = (__nv_fp8x2_storage_t)(w[i >> 1] >> (16 * (i & 1)));
+    const float2 f = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3)));
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+
+template <typename TQ, typename TK>
+__global__ void __launch_bounds__(kThreads, 2) kweights_simt_kernel(const KwParams p) {
+  __shared__ __align__(16) float sK[2][kBK][kPitch];
+  __shared__ __align__(16) float sQ[2][kBK][kPitch];
+  __shared__ float sLse[kKwRows];
+  __shared__ uint64_t sMask[kKwRows][2];
+  __shared__ float sSum[kThreads / 16][kKwKeys];
+  const int tid = threadIdx.x;
+  const int b = blockIdx.y, split = blockIdx.z, j0 = blockIdx.x * kKwKeys;
+  const KwRequest rq = kw_request(p, b);
+  if (!rq.ok || j0 >= rq.kv_len) {
+    if (!rq.ok && blockIdx.x == 0 && split == 0 && tid == 0 && p.req_status)
+      p.req_status[b] = VA_ERR_INVALID_ARG;
+    return;
+  }
+  const int P = rq.kv_len - p.T;
+  if (rq.bad_accept && blockIdx.x == 0 && split == 0 && tid == 0 && p.req_status)
+    p.req_status[b] = VA_ERR_INVALID_ARG;
+  const int R = rq.nodes * p.H;
+  const int blocks = (R + kKwRows - 1) / kKwRows;
+  const int blk0 = (int)((long long)blocks * split / p.splits);
+  const int blk1 = (int)((long long)blocks * (split + 1) / p.splits);
+
+  // this thread stages key (and row) tid & 127, dims 8 (tid >> 7) .. +7 of a step
+  const int sr = tid & 127, sd = (tid >> 7) * 8;
+  const int key = j0 + sr;
+  const int krow = kw_pool_row(p, b, rq.kv_len, key);
+  if (krow < 0 && key < rq.kv_len && split == 0 && p.req_status)
+    p.req_status[b] = VA_ERR_INVALID_ARG;  // page index out of range
+  const TK* kc = reinterpret_cast<const TK*>(p.c_kv) + (size_t)max(krow, 0) * kDc;
+  const TK* kp = reinterpret_cast<const TK*>(p.k_pe) + (size_t)max(krow, 0) * kDr;
+  const int tx = tid & 15, ty = tid >> 4;
+  float ksum[8] = {};
+
+  for (int blk = blk0; blk < blk1; ++blk) {
+    const int row = blk * kKwRows + sr;
+    int node;
+    const int g = kw_query_row(p, b, rq, row, &node);  // -1: adds nothing
+    const TQ* qn = reinterpret_cast<const TQ*>(p.q_nope) + (size_t)max(g, 0) * kDc;
+    const TQ* qp = reinterpret_cast<const TQ*>(p.q_pe) + (size_t)max(g, 0) * kDr;
+    if (tid < kKwRows) kw_row_info(p, b, g, node, &sLse[sr], sMask[sr]);
+
+    float fk[8], fq[8];
+    auto fetch = [&](int d0) {
+      const int d = d0 + sd;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) fk[i] = fq[i] = 0.f;
+      if (krow >= 0) {
+        if (d < kDc) load8(kc + d, fk); else load8(kp + d - kDc, fk);
+      }
+      if (g >= 0) {
+        if (d < kDc) load8(qn + d, fq); else load8(qp + d - kDc, fq);
+      }
+    };
+    auto put = [&](int buf) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        sK[buf][sd + i][sr] = fk[i];
+        sQ[buf][sd + i][sr] = fq[i];
+      }
+    };
+    float acc[8][8] = {};  // [row][key]
+    fetch(0);
+    put(0);
+    __syncthreads();
+    for (int s = 0; s < kDqk / kBK; ++s) {
+      if (s + 1 < kDqk / kBK) fetch((s + 1) * kBK);
+      const int cur = s & 1;
+#pragma unroll
+      for (int d = 0; d < kBK; ++d) {
+        float k[8], q[8];
+        *reinterpret_cast<float4*>(&k[0]) = *reinterpret_cast<float4*>(&sK[cur][d][tx * 4]);
+        *reinterpret_cast<float4*>(&k[4]) = *reinterpret_cast<float4*>(&sK[cur][d][64 + tx * 4]);
+        *reinterpret_cast<float4*>(&q[0]) = *reinterpret_cast<float4*>(&sQ[cur][d][ty * 4]);
+        *reinterpret_cast<float4*>(&q[4]) = *reinterpret_cast<float4*>(&sQ[cur][d][64 + ty * 4]);
+#pragma unroll
+        for (int r = 0; r < 8; ++r)
+#pragma unroll
+          for (int c = 0; c < 8; ++c) acc[r][c] = fmaf(q[r], k[c], acc[r][c]);
+      }
+      if (s + 1 < kDqk / kBK) put(cur ^ 1);
+      __syncthreads();
+    }
+    const bool tail = j0 + kKwKeys > P;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const int rr = (r < 4 ? 0 : 60) + ty * 4 + r;
+      const float l = sLse[rr];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        const int kk = (c < 4 ? 0 : 60) + tx * 4 + c;
+        float w = ex2f(fmaf(acc[r][c], p.scale, -l) * kLog2e);
+        if (tail) {
+          const int nd = j0 + kk - P;
+          if (nd >= 0 && !(nd < p.T && ((sMask[rr][nd >> 6] >> (nd & 63)) & 1ull))) w = 0.f;
+        }
+        ksum[c] += w;
+      }
+    }
+    __syncthreads();  // sLse and sMask are rewritten by the next block
+  }
+
+#pragma unroll
+  for (int c = 0; c < 8; ++c) sSum[ty][(c < 4 ? 0 : 60) + tx * 4 + c] = ksum[c];
+  __syncthreads();
+  if (tid < kKwKeys && key < rq.kv_len) {
+    float w = 0.f;
+#pragma unroll
+    for (int y = 0; y < kThreads / 16; ++y) w += sSum[y][tid];
+    kw_store(p, b, split, key, krow >= 0 ? w : 0.f);
+  }
+}
+
+// Adds the splits' partial sums, in split order, to the decayed weights.
+__global__ void __launch_bounds__(256) kweights_join_kernel(const KwParams p) {
+  const int b = blockIdx.y;
+  const int j = blockIdx.x * 256 + threadIdx.x;
+  const KwRequest rq = kw_request(p, b);
+  if (!rq.ok || j >= rq.kv_len) return;
+  const size_t cap = (size_t)p.max_pages * kPage;
+  float w = 0.f;
+  for (int s = 0; s < p.splits; ++s) w += p.part[((size_t)s * p.B + b) * cap + j];
+  const size_t at = (size_t)b * cap + j;
+  p.weights[at] = (p.weights_in ? p.decay * p.weights_in[at] : 0.f) + w;
+}
+
+}  // namespace
+
+cudaError_t launch_kweights_join(const KwParams& p, cudaStream_t st) {
+  const dim3 grid((unsigned)((p.max_pages * kPage + 255) / 256), (unsigned)p.B);
+  kweights_join_kernel<<<grid, 256, 0, st>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_kweights_simt(const va_key_weight_args& a, const KwParams& p, cudaStream_t st) {
+  const dim3 grid((unsigned)((p.max_pages * kPage + kKwKeys - 1) / kKwKeys), (unsigned)p.B,
+                  (unsigned)p.splits);
+  const bool fp8 = a.flags & VA_FLAG_KV_FP8_E4M3;
+  if (a.dtype == VA_F32) {
+    if (fp8) kweights_simt_kernel<float, __nv_fp8_e4m3><<<grid, kThreads, 0, st>>>(p);
+    else kweights_simt_kernel<float, float><<<grid, kThreads, 0, st>>>(p);
+  } else {
+    if (fp8) kweights_simt_kernel<__nv_bfloat16, __nv_fp8_e4m3><<<grid, kThreads, 0, st>>>(p);
+    else kweights_simt_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, kThreads, 0, st>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace va

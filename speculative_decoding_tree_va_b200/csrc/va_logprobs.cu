@@ -1,0 +1,435 @@
+// Log probabilities of given tokens, entropy and top alternatives of rows of
+// logits: the drafter's per-depth top-k and the target's greedy tokens.
+//
+// With m the row's maximum, c = scale log2(e) and y_v = c (x_v - m) <= 0:
+//   Z = sum 2^y_v     S = sum 2^y_v y_v
+//   lse = scale m + ln Z     lp_v = scale (x_v - m) - ln Z
+//   entropy = ln2 (log2 Z - S / Z)
+// x - m is taken before it is scaled: exact near the maximum, and a row whose
+// logits are all the type's lowest value still has differences of 0.  A
+// thread holds (m, Z, S) of what it has read and rescales them once per tile.
+//
+// Top K: a candidate is a 64-bit key, the logit in order-preserving bits over
+// the complement of its index, so that equal logits order by lower index.
+// The K-th largest of the threads' maxima over the first tile is a lower
+// bound of the row's K-th logit; a thread whose tile maximum reaches the bound
+// pushes the elements that do into a shared buffer, which is cut down to
+// its K largest (and the bound raised) when it holds more than kLimit.
+//
+// Bound by the one read of the logits from HBM.
+#include <cfloat>
+
+#include "va_common.cuh"
+
+namespace va {
+namespace {
+
+constexpr int kNT = 256;     // threads per CTA
+constexpr int kU = 4;        // 16-byte vectors a thread holds per tile
+constexpr int kLimit = 256;  // candidates kept before they are cut down
+constexpr int kMaxCluster = 8;
+constexpr unsigned kFull = 0xffffffffu;
+constexpr float kFloor = -1.0e4f;  // 2^kFloor = 0; keeps 0 * y finite
+
+struct LpParams {
+  const void* logits;
+  const int32_t* tokens;
+  long long ld;
+  int V, G, K;
+  float scale;
+  float* lse;
+  float* entropy;
+  float* tok_lp;
+  int32_t* top_ids;
+  float* top_lp;
+  double* top_lp64;
+  int32_t* row_status;
+};
+
+__device__ __forceinline__ float ex2f(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// max that keeps a NaN of either operand
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+// Bits that order like the value (-0 like +0); NaN never reaches the output.
+__device__ __forceinline__ uint32_t order_bits(float x) {
+  const uint32_t u = __float_as_uint(x + 0.0f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+__device__ __forceinline__ float order_value(uint32_t o) {
+  return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
+}
+__device__ __forceinline__ uint64_t make_key(float x, int idx) {
+  return ((uint64_t)order_bits(x) << 32) | (uint32_t)~idx;
+}
+__device__ __forceinline__ int key_index(uint64_t k) { return (int)~(uint32_t)k; }
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;"
+               ::: "memory");
+}
+// Address of `p` (this CTA's shared memory) in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t remote(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(r) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float remote_f32(const float* p, uint32_t rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint64_t remote_u64(const uint64_t* p, uint32_t rank) {
+  uint64_t v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(remote(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 load_stream(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+template <typename T> struct Vec;  // a 16-byte vector of logits
+template <> struct Vec<float> {
+  static constexpr int N = 4;
+  static __device__ __forceinline__ void unpack(const uint4& v, float (&x)[4]) {
+    x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y);
+    x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
+  }
+  static __device__ __forceinline__ uint32_t bits(float x) { return __float_as_uint(x); }
+  static constexpr uint32_t kNegInf = 0xff800000u;
+};
+template <> struct Vec<__nv_bfloat16> {
+  static constexpr int N = 8;
+  static __device__ __forceinline__ void unpack(const uint4& v, float (&x)[8]) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = __uint_as_float(w[i] << 16);
+      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  static constexpr uint32_t kNegInf = 0xff80ff80u;
+};
+
+// Online sums of one thread: maximum, Z and S relative to it.
+struct Sums {
+  float m = -FLT_MAX, z = 0.f, s = 0.f;
+  __device__ __forceinline__ void raise(float to, float c) {  // to >= m, or NaN
+    const float d = max_nan((m - to) * c, kFloor);
+    const float f = ex2f(d);
+    s = f * fmaf(z, d, s);
+    z *= f;
+    m = to;
+  }
+  __device__ __forceinline__ void add(float x, float c) {
+    const float y = max_nan((x - m) * c, kFloor);
+    const float e = ex2f(y);
+    z += e;
+    s = fmaf(e, y, s);
+  }
+  __device__ __forceinline__ void join(const Sums& o, float c) {
+    Sums a = *this, b = o;
+    const float to = max_nan(a.m, b.m);
+    a.raise(to, c);
+    b.raise(to, c);
+    m = to;
+    z = a.z + b.z;
+    s = a.s + b.s;
+  }
+};
+
+// Cuts cand[0, n) to its K largest keys, descending, in cand[0, K) (0 where
+// there are fewer).  Called by the whole CTA; all keys are distinct.
+__device__ void cut_down(uint64_t* cand, int n, int K, uint64_t* tmp) {
+  const int tid = threadIdx.x;
+  if (tid < VA_MAX_TOPK) tmp[tid] = 0;
+  __syncthreads();
+  if (n <= kNT) {  // rank of each key among all
+    if (tid < n) {
+      const uint64_t k = cand[tid];
+      int r = 0;
+      for (int i = 0; i < n; ++i) r += cand[i] > k;
+      if (r < K) tmp[r] = k;
+    }
+  } else {  // crowded (many equal logits): K rounds of the largest key below the last
+    __shared__ unsigned long long best;
+    uint64_t below = ~0ull;
+    for (int r = 0; r < K; ++r) {
+      if (tid == 0) best = 0;
+      __syncthreads();
+      unsigned long long mine = 0;
+      for (int i = tid; i < n; i += kNT)
+        if (cand[i] < below && cand[i] > mine) mine = cand[i];
+      if (mine) atomicMax(&best, mine);
+      __syncthreads();
+      below = best;
+      if (tid == 0) tmp[r] = below;
+      __syncthreads();
+      if (below == 0) break;
+    }
+  }
+  __syncthreads();
+  if (tid < K) cand[tid] = tmp[tid];
+  __syncthreads();
+}
+
+// One row per cluster: CTA `rank` of C reads the rank-th part of the row's
+// vectors, rank 0 joins the parts over distributed shared memory.
+template <typename T>
+__global__ void __launch_bounds__(kNT) logprobs_kernel(const LpParams p, int C) {
+  using VT = Vec<T>;
+  constexpr int N = VT::N;
+  extern __shared__ uint64_t cand[];  // kLimit + a tile's kNT * kU * N keys
+  __shared__ uint64_t tmp[VA_MAX_TOPK];
+  __shared__ float wm[kNT / 32], wz[kNT / 32], ws[kNT / 32];
+  __shared__ float part[3];           // this CTA's sums
+  __shared__ float tmax[kNT];
+  __shared__ int count;
+  __shared__ float bound;
+  __shared__ float fin[2];            // the row's maximum and ln Z
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t rank = C > 1 ? cluster_rank() : 0;
+  const long long row = blockIdx.x / C;
+  const int V = p.V, K = p.K;
+  const T* x0 = reinterpret_cast<const T*>(p.logits) + row * p.ld;
+  // vectors are taken at 16-byte boundaries: element v of the row is element
+  // v + off of the aligned base, and only a row's first and last vector may
+  // reach past it (those are read element by element)
+  const int off = (int)(((uintptr_t)x0 & 15) / sizeof(T));
+  const T* base = x0 - off;
+  const int nv = (int)(((long long)V + off + N - 1) / N);
+  const int per = (nv + C - 1) / C;
+  const int v0 = min(nv, (int)rank * per), v1 = min(nv, v0 + per);
+  const float c = p.scale * kLog2e;
+
+  if (tid == 0) { count = 0; bound = -INFINITY; }
+  __syncthreads();
+
+  Sums acc;
+  bool first = true;
+  for (int t0 = v0; t0 < v1; t0 += kNT * kU) {
+    uint4 raw[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      const int j = t0 + u * kNT + tid;
+      if (j < v1 && (j > 0 || off == 0) && (long long)(j + 1) * N - off <= V) {
+        raw[u] = load_stream(reinterpret_cast<const uint4*>(base) + j);
+      } else {
+        raw[u] = make_uint4(VT::kNegInf, VT::kNegInf, VT::kNegInf, VT::kNegInf);
+        if (j < v1) {
+          T e[N];
+          *reinterpret_cast<uint4*>(e) = raw[u];
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            const long long v = (long long)j * N + i - off;
+            if (v >= 0 && v < V) e[i] = x0[v];
+          }
+          raw[u] = *reinterpret_cast<uint4*>(e);
+        }
+      }
+    }
+    float mt = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      float x[N];
+      VT::unpack(raw[u], x);
+#pragma unroll
+      for (int i = 0; i < N; ++i) mt = max_nan(mt, x[i]);
+    }
+    if (!(mt <= acc.m)) acc.raise(mt, c);
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      float x[N];
+      VT::unpack(raw[u], x);
+#pragma unroll
+      for (int i = 0; i < N; ++i) acc.add(x[i], c);
+    }
+    if (K > 0) {
+      if (first) {
+        // the K-th largest thread maximum (ties by thread) bounds the K-th logit
+        tmax[tid] = mt;
+        __syncthreads();
+        const uint32_t mine = order_bits(mt);
+        int r = 0;
+        for (int i = 0; i < kNT; ++i) {
+          const uint32_t o = order_bits(tmax[i]);
+          r += o > mine || (o == mine && i < tid);
+        }
+        if (r == K - 1 && mt > -INFINITY) bound = mt;
+        __syncthreads();
+        first = false;
+      }
+      bool full = false;
+      const float b = bound;
+      if (mt >= b) {
+#pragma unroll
+        for (int u = 0; u < kU; ++u) {
+          float x[N];
+          VT::unpack(raw[u], x);
+          const long long at = (long long)(t0 + u * kNT + tid) * N - off;
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            if (x[i] >= b && t0 + u * kNT + tid < v1 && at + i >= 0 && at + i < V) {
+              const int n = atomicAdd(&count, 1);
+              cand[n] = make_key(x[i], (int)(at + i));
+              full |= n >= kLimit;
+            }
+          }
+        }
+      }
+      if (__syncthreads_or(full)) {
+        cut_down(cand, count, K, tmp);
+        if (tid == 0) {
+          count = K;
+          bound = order_value((uint32_t)(cand[K - 1] >> 32));
+        }
+        __syncthreads();
+      }
+    }
+  }
+  if (K > 0) cut_down(cand, count, K, tmp);
+
+  // join the threads' sums: lanes, then warps
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    Sums o;
+    o.m = __shfl_xor_sync(kFull, acc.m, d);
+    o.z = __shfl_xor_sync(kFull, acc.z, d);
+    o.s = __shfl_xor_sync(kFull, acc.s, d);
+    acc.join(o, c);
+  }
+  if (lane == 0) { wm[warp] = acc.m; wz[warp] = acc.z; ws[warp] = acc.s; }
+  __syncthreads();
+  if (tid == 0) {
+    Sums a;
+    for (int w = 0; w < kNT / 32; ++w) {
+      Sums o;
+      o.m = wm[w]; o.z = wz[w]; o.s = ws[w];
+      a.join(o, c);
+    }
+    part[0] = a.m; part[1] = a.z; part[2] = a.s;
+  }
+  if (C > 1) {
+    cluster_sync_all();  // every CTA's part[] and cand[0, K) are in place
+    if (rank == 0) {
+      if (tid == 0) {
+        Sums a;
+        for (int r = 0; r < C; ++r) {
+          Sums o;
+          o.m = remote_f32(&part[0], r);
+          o.z = remote_f32(&part[1], r);
+          o.s = remote_f32(&part[2], r);
+          a.join(o, c);
+        }
+        part[0] = a.m; part[1] = a.z; part[2] = a.s;
+      }
+      if (tid >= K && tid < C * K) cand[tid] = remote_u64(&cand[tid % K], tid / K);
+    }
+    cluster_sync_all();  // remote reads are done: the other CTAs may exit
+    if (rank != 0) return;
+    if (K > 0) cut_down(cand, C * K, K, tmp);
+  }
+  __syncthreads();
+  if (tid == 0) {
+    const float m = part[0], z = part[1];
+    const bool bad = !(z == z) || m == INFINITY;
+    const float lnz = logf(z);  // z = 0 (no finite logit): -inf
+    fin[0] = m;
+    fin[1] = bad ? NAN : lnz;
+    if (p.lse) p.lse[row] = bad ? NAN : (z > 0.f ? fmaf(m, p.scale, lnz) : -INFINITY);
+    if (p.entropy)
+      p.entropy[row] = bad ? NAN : (z > 0.f ? fmaxf(lnz - kLn2 * (part[2] / z), 0.f) : 0.f);
+    if (bad && p.row_status) p.row_status[row] = VA_ERR_INVALID_ARG;
+  }
+  __syncthreads();
+  const float m = fin[0], lnz = fin[1];
+  const bool bad = !(lnz == lnz);
+  const bool none = lnz == -INFINITY;
+  for (int g = tid; g < p.G; g += kNT) {
+    const int t = p.tokens[row * p.G + g];
+    float lp = -INFINITY;
+    if (t >= V) {
+      lp = NAN;
+      if (p.row_status) p.row_status[row] = VA_ERR_INVALID_ARG;
+    } else if (t >= 0 && !none) {
+      lp = fmaf(to_f32(x0[t]) - m, p.scale, -lnz);
+    }
+    p.tok_lp[row * p.G + g] = bad ? NAN : lp;
+  }
+  if (tid < K) {
+    const uint64_t k = cand[tid];
+    const float x = order_value((uint32_t)(k >> 32));
+    float lp = none ? -INFINITY : fmaf(x - m, p.scale, -lnz);
+    if (bad) lp = NAN;
+    p.top_ids[row * K + tid] = bad || k == 0 ? -1 : key_index(k);
+    if (p.top_lp) p.top_lp[row * K + tid] = lp;
+    if (p.top_lp64) p.top_lp64[row * K + tid] = (double)lp;
+  }
+}
+
+template <typename T>
+cudaError_t launch(const LpParams& p, int R, int C, cudaStream_t st) {
+  constexpr int kCandBytes = (kLimit + kNT * kU * Vec<T>::N) * (int)sizeof(uint64_t);
+  const size_t smem = p.K > 0 ? kCandBytes : 0;
+  if (smem > 40 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(logprobs_kernel<T>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kCandBytes);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = C;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((long long)R * C));
+  cfg.blockDim = dim3(kNT);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = at;
+  cfg.numAttrs = C > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, logprobs_kernel<T>, p, C);
+}
+
+}  // namespace
+
+cudaError_t launch_logprobs(const va_logprob_args& a, int sms, cudaStream_t st) {
+  LpParams p;
+  p.logits = a.logits;
+  p.tokens = a.tokens;
+  p.ld = a.ld;
+  p.V = a.V;
+  p.G = a.G;
+  p.K = a.K;
+  p.scale = a.scale;
+  p.lse = a.lse;
+  p.entropy = a.entropy;
+  p.tok_lp = a.tok_lp;
+  p.top_ids = a.top_ids;
+  p.top_lp = a.top_lp;
+  p.top_lp64 = a.top_lp64;
+  p.row_status = a.row_status;
+  // Few rows: a row is cut over a cluster while its CTAs keep more than one
+  // tile each and the SMs are not yet covered.
+  const long long tile = (long long)kNT * kU * (a.dtype == VA_F32 ? 4 : 8);
+  int C = 1;
+  while (C < kMaxCluster && (long long)a.R * C < sms && (long long)a.V > tile * C) C *= 2;
+  return a.dtype == VA_F32 ? launch<float>(p, a.R, C, st) : launch<__nv_bfloat16>(p, a.R, C, st);
+}
+
+}  // namespace va
