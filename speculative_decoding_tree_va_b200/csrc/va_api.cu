@@ -138,7 +138,12 @@ int check_key_weights(const va_key_weight_args* a) {
 // would leave SMs idle.  With an accepted path the host does not know its
 // length: a path of the deepest tree is assumed, and splits without rows only
 // write zeros.
+bool key_weights_on_tc(const va_key_weight_args* a) {
+  return a->dtype == VA_BF16 && !(a->flags & VA_FLAG_BF16_CUDA_CORES);
+}
+
 int key_weight_splits(const va_key_weight_args* a) {
+  if (key_weights_on_tc(a)) return 1;
   const int sms = sm_count();
   const int nodes = a->path && a->T > VA_MAX_DEPTH + 1 ? VA_MAX_DEPTH + 1 : a->T;
   const long long blocks = ((long long)nodes * a->H + va::kKwRows - 1) / va::kKwRows;
@@ -151,6 +156,7 @@ int key_weight_splits(const va_key_weight_args* a) {
 }
 
 size_t key_weight_workspace(const va_key_weight_args* a, int splits) {
+  if (key_weights_on_tc(a)) return va::kweights_tc_workspace(*a);
   if (splits < 2) return 0;
   return va::align256((size_t)splits * a->B * a->max_pages * VA_PAGE_SIZE * sizeof(float));
 }
@@ -388,7 +394,7 @@ int va_key_weights(const va_key_weight_args* args, va_stream_t stream) {
   p.accept_len = args->accept_len;
   p.weights_in = args->weights_in;
   p.weights = args->weights;
-  p.part = need ? static_cast<float*>(args->workspace) : nullptr;
+  p.part = splits > 1 ? static_cast<float*>(args->workspace) : nullptr;
   p.req_status = args->req_status;
   p.B = args->B;
   p.H = args->H;
@@ -398,7 +404,9 @@ int va_key_weights(const va_key_weight_args* args, va_stream_t stream) {
   p.splits = splits;
   p.scale = (args->flags & VA_FLAG_KV_FP8_E4M3) ? args->scale * args->kv_scale : args->scale;
   p.decay = args->decay;
-  cudaError_t e = va::launch_kweights_simt(*args, p, (cudaStream_t)stream);
+  cudaError_t e;
+  if (key_weights_on_tc(args)) e = va::launch_kweights_tc(*args, p, sm_count(), (cudaStream_t)stream);
+  else e = va::launch_kweights_simt(*args, p, (cudaStream_t)stream);
   if (e == cudaSuccess && splits > 1) e = va::launch_kweights_join(p, (cudaStream_t)stream);
   return e == cudaSuccess ? VA_OK : VA_ERR_CUDA;
 }
@@ -446,9 +454,9 @@ int va_kv_move(void* c_kv, void* k_pe, int elem_bytes, int num_pages, int page_s
 }
 
 unsigned int va_device_timeouts(void) {
-  const unsigned int a = va::tc_timeouts(), b = va::simt_timeouts();
-  if (a == 0xFFFFFFFFu || b == 0xFFFFFFFFu) return 0xFFFFFFFFu;
-  return a + b;
+  const unsigned int a = va::tc_timeouts(), b = va::simt_timeouts(), c = va::kw_timeouts();
+  if (a == 0xFFFFFFFFu || b == 0xFFFFFFFFu || c == 0xFFFFFFFFu) return 0xFFFFFFFFu;
+  return a + b + c;
 }
 
 }  // extern "C"

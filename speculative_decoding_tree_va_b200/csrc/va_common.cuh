@@ -169,6 +169,7 @@ cudaError_t launch_tree_mask(const int32_t* parents, int B, int T, uint64_t* mas
 // (0xFFFFFFFF if the counter cannot be read).
 unsigned int tc_timeouts();
 unsigned int simt_timeouts();
+unsigned int kw_timeouts();  // the key-weight kernel's
 
 cudaError_t launch_attn_simt(const va_attn_args& a, SplitRange sp, float* o_part,
                              float* lse_part, cudaStream_t st, const Balance& bal);

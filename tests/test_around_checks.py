@@ -63,7 +63,7 @@ def key_weight_args(**kw):
 def test_key_weight_checks(lib, bad, status):
     a = key_weight_args(**bad)
     if "workspace" in bad or "workspace_bytes" in bad:  # a call that needs one
-        a.B, a.max_pages = 1, 2
+        a.B, a.max_pages, a.dtype = 1, 2, va.VA_F32
         assert lib.va_key_weights_workspace_bytes(ctypes.byref(a)) > 16
     assert lib.va_key_weights(ctypes.byref(a), None) == status
     if status != 1 or "workspace" not in str(bad):
