@@ -43,9 +43,8 @@ constexpr int kQSlots = 4;
 constexpr int kQSlot = 128 * 128;       // bytes: up to 128 rows x 64 dims
 constexpr int kQBytes = kChunks * 64 * 128;  // resident rows: 64 a CTA (>= the ring)
 constexpr int kRowsResident = 128;      // of the pair
-constexpr int kEpiThreads = 256;
-constexpr int kWarpK = 0, kWarpMma = 1, kWarpEpi = 2, kWarpQ = 10, kWarpConv = 11;
-constexpr int kConvWarps = 4;          // one key of the CTA's tile per thread
+constexpr int kWarpK = 0, kWarpMma = 1, kWarpEpi = 2, kWarpQ = 10, kWarpInfo = 11, kWarpConv = 12;
+constexpr int kConvWarps = 8;          // 16 keys of the CTA's tile each
 constexpr int kConvAhead = 4;           // chunks whose codes are in flight
 static_assert(kQBytes >= kQSlots * kQSlot, "the ring shares the resident rows' space");
 
@@ -61,17 +60,22 @@ struct __align__(16) Ctl {
   uint64_t q_full[kQSlots], q_empty[kQSlots];
   uint64_t r_full, r_empty;   // resident rows
   uint64_t s_full[2], s_empty[2];
+  uint64_t i_full[2], i_empty[2];  // column data of a pass
   uint64_t drain;
   long long start_off, lo, hi;
   int start_b, start_tile;
   uint32_t tmem;
   int abort;
-  uint32_t inv[2][8];         // columns of a 32-column group that add nothing
+  // of each column of a pass: its node, its row's log2-sum and factor; and one
+  // bit where the column adds nothing (no row, absent node, empty row)
+  uint32_t none[2][8];
+  int one[2][8];         // the node of all that a 32-column group adds, or -1
   float xsum[2][128];
   uint8_t node[2][256];
-  float2 col[2][256];         // factor and log2-sum of a column's row
+  float l2[2][256];
+  float factor[2][256];  // FP8 cache
 };
-constexpr int kScanAt = offsetof(Ctl, xsum);  // the start-up scan uses xsum .. col
+constexpr int kScanAt = offsetof(Ctl, xsum);  // the start-up scan uses xsum ..
 static_assert(kScanAt % 8 == 0, "scan alignment");
 constexpr size_t kSmemBytes = 1024 + (size_t)kChunks * kKChunk + kQBytes + sizeof(Ctl);
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
@@ -164,6 +168,8 @@ kweights_tc_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_const
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c.s_full[i], 1);
       mbar_init(&c.s_empty[i], 16);  // 8 epilogue warps x 2 CTAs
+      mbar_init(&c.i_full[i], 1);
+      mbar_init(&c.i_empty[i], 8);
     }
     mbar_init(&c.drain, 1);
     c.abort = 0;
@@ -403,108 +409,144 @@ kweights_tc_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_const
     }
   } else if (F8 && warp >= kWarpConv) {
     // ------------------------------------------- key chunks from FP8 codes, as fp16
-    // Thread m converts key m of the tile; the codes of the next kConvAhead chunks
-    // (64 bytes each) are in flight in registers.
-    const int m = tid - kWarpConv * 32;
-    const uint8_t* ckv = reinterpret_cast<const uint8_t*>(p.c_kv);
-    const uint8_t* kpe = reinterpret_cast<const uint8_t*>(p.k_pe);
-    uint4 code[kChunks][4];
-    auto fetch = [&](int kc, int row) {
-      const uint4* src = reinterpret_cast<const uint4*>(kc < 8 ? ckv + (size_t)max(row, 0) * kDc + kc * 64
-                                                               : kpe + (size_t)max(row, 0) * kDr);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) code[kc][i] = row >= 0 ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+    // A warp converts 16 keys of one page.  Of a chunk, lane l reads 16 codes (l & 3)
+    // of keys l / 4 + 8 i, so that 4 lanes read a key's 64 bytes; the codes of the
+    // next kConvAhead chunks are in flight in registers (volatile: loads stay there).
+    const int m0 = (warp - kWarpConv) * 16, sub = lane >> 2, u0 = lane & 3;
+    const uint8_t* ckv = reinterpret_cast<const uint8_t*>(p.c_kv) + u0 * 16;
+    const uint8_t* kpe = reinterpret_cast<const uint8_t*>(p.k_pe) + u0 * 16;
+    uint4 code[kChunks][2];
+    // pool row of the warp's first key, and how many of its keys exist
+    struct Keys { int row, n; };
+    auto keys_of = [&](const Walk& v) {
+      Keys k{0, 0};
+      if (!v.alive()) return k;
+      const int key = v.tile * kTileKeys + (int)rank * 128 + m0;
+      const int row = kw_pool_row(p, v.b, v.kv_len, key);
+      if (row >= 0) { k.row = row; k.n = v.kv_len - key; }
+      return k;
     };
-    auto row_of = [&](const Walk& v) {
-      return v.alive() ? kw_pool_row(p, v.b, v.kv_len, v.tile * kTileKeys + (int)rank * 128 + m) : -1;
+    auto fetch = [&](int kc, const Keys& k) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint4& v = code[kc][i];
+        v = make_uint4(0, 0, 0, 0);
+        const int r = sub + 8 * i;
+        const uint8_t* src = kc < 8 ? ckv + (size_t)(k.row + r) * kDc + kc * 64
+                                    : kpe + (size_t)(k.row + r) * kDr;
+        if (r < k.n)
+          asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(src));
+      }
     };
     const uint32_t full0 = map_to_rank(smem_u32(&c.k_full[0]), 0);
-    int row = row_of(w);
+    Keys keys = keys_of(w);
 #pragma unroll
-    for (int kc = 0; kc < kConvAhead; ++kc) fetch(kc, row);
+    for (int kc = 0; kc < kConvAhead; ++kc) fetch(kc, keys);
     uint32_t phase = 0;
     bool go = true;
     while (w.alive() && go) {
       w.next();
-      const int row_next = row_of(w);
+      const Keys next = keys_of(w);
 #pragma unroll
       for (int kc = 0; kc < kChunks; ++kc) {
-        if (kc + kConvAhead < kChunks) fetch(kc + kConvAhead, row);
-        else fetch(kc + kConvAhead - kChunks, row_next);
+        if (kc + kConvAhead < kChunks) fetch(kc + kConvAhead, keys);
+        else fetch(kc + kConvAhead - kChunks, next);
         if (go) go = warp_wait(&c.k_empty[kc], phase ^ 1, abort, expired);
-        uint8_t* dst = sK + (size_t)kc * kKChunk + m * 128;
+        uint8_t* dst = sK + (size_t)kc * kKChunk + m0 * 128;
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {  // 8 codes -> 16 bytes
-          const uint4& v = code[kc][u >> 1];
-          const uint32_t w0 = (u & 1) ? v.z : v.x, w1 = (u & 1) ? v.w : v.y;
-          uint32_t o[4];
+        for (int i = 0; i < 2; ++i) {
+          const int r = sub + 8 * i;
+          const uint32_t cw[4] = {code[kc][i].x, code[kc][i].y, code[kc][i].z, code[kc][i].w};
+          uint32_t o[8];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t two = ((i & 2) ? w1 : w0) >> (16 * (i & 1));
-            const __half2_raw f = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-            o[i] = (uint32_t)f.x | (uint32_t)f.y << 16;
+          for (int j = 0; j < 8; ++j) {
+            const __half2_raw f = __nv_cvt_fp8x2_to_halfraw2(
+                (__nv_fp8x2_storage_t)(cw[j >> 1] >> (16 * (j & 1))), __NV_E4M3);
+            o[j] = (uint32_t)f.x | (uint32_t)f.y << 16;
           }
-          *reinterpret_cast<uint4*>(dst + ((u ^ (m & 7)) << 4)) =
+          uint8_t* row = dst + r * 128;
+          *reinterpret_cast<uint4*>(row + (((2 * u0) ^ (r & 7)) << 4)) =
               make_uint4(o[0], o[1], o[2], o[3]);
+          *reinterpret_cast<uint4*>(row + (((2 * u0 + 1) ^ (r & 7)) << 4)) =
+              make_uint4(o[4], o[5], o[6], o[7]);
         }
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) arrive_cluster(full0 + kc * 8);
       }
-      row = row_next;
+      keys = next;
       phase ^= 1;
     }
     for (int kc = 0; kc < kChunks && go; ++kc)
       go = warp_wait(&c.k_empty[kc], phase ^ 1, abort, expired);
+  } else if (warp == kWarpInfo) {
+    // ------------------------------------------------------- column data of each pass
+    // One pass ahead of the epilogue, so that its loads are off the epilogue's path.
+    const int W = (p.T + 63) >> 6;
+    uint32_t pass = 0;
+    bool go = true;
+    for (; w.alive() && go; w.next()) {
+      const int blocks = row_blocks(w.R);
+      for (int rb = 0; rb < blocks && go; ++rb, ++pass) {
+        const int buf = pass & 1;
+        float l[8], f[8];
+        uint64_t word[8];
+        int node[8];
+        bool ok[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const int r = rb * 256 + k * 32 + lane;
+          const bool in = r < w.R;
+          const int i = in ? r / p.H : 0;
+          const int n = in && p.path ? p.path[(size_t)w.b * p.T + i] : i;
+          ok[k] = in && n >= 0 && n < p.T;
+          if (in && !ok[k] && p.req_status) p.req_status[w.b] = VA_ERR_INVALID_ARG;
+          node[k] = ok[k] ? n : 0;
+          const size_t row = (size_t)w.b * p.T + node[k];
+          word[k] = p.tree_mask[row * W + (node[k] >> 6)];
+          l[k] = p.lse[ok[k] ? row * p.H + (r - i * p.H) : 0];
+          f[k] = F8 && ok[k] ? tp.q_scale[(size_t)w.b * p.T * p.H + r] : 0.f;
+        }
+        go = warp_wait(&c.i_empty[buf], ((pass >> 1) & 1) ^ 1, abort, expired);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const bool adds = ok[k] && ((word[k] >> (node[k] & 63)) & 1ull) && l[k] != -INFINITY;
+          const int e = k * 32 + lane;
+          c.node[buf][e] = (uint8_t)node[k];
+          c.l2[buf][e] = l[k] * kLog2e;
+          if (F8) c.factor[buf][e] = adds ? f[k] * (p.scale * kLog2e) : 0.f;
+          const uint32_t none = __ballot_sync(0xffffffffu, !adds);
+          const int first = __shfl_sync(0xffffffffu, node[k], none == ~0u ? 0 : __ffs(~none) - 1);
+          const bool same = __all_sync(0xffffffffu, !adds || node[k] == first);
+          if (lane == 0) {
+            c.none[buf][k] = none;
+            c.one[buf][k] = same ? first : -1;
+          }
+        }
+        __syncwarp();
+        if (lane == 0)
+          asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&c.i_full[buf]))
+                       : "memory");
+      }
+    }
   } else if (warp >= kWarpEpi && warp < kWarpQ) {
     // ----------------------------------------------------------- exponentials, sums
     // Warp w reads lane quadrant w & 3 (keys 32 (w & 3) .. of this CTA); the two
     // warps of a quadrant take the two halves of a pass's columns.
-    const int e = tid - kWarpEpi * 32;
-    const int q = warp & 3, half = e >> 7, m = 32 * q + lane;
+    const int q = warp & 3, half = (warp - kWarpEpi) >> 2, m = 32 * q + lane;
     const uint32_t lane_base = (uint32_t)(32 * q) << 16;
     const uint32_t free0 = map_to_rank(smem_u32(&c.s_empty[0]), 0);
     const float factor = p.scale * kLog2e;
-    // a column's row: factor, log2-sum and node, for the pass after this one
     const int W = (p.T + 63) >> 6;
-    float2 col = make_float2(factor, 0.f);
-    int node = 0;
-    bool adds = false;
-    auto column = [&](const Walk& v, int rb) {
-      adds = false;
-      if (!v.alive()) return;
-      // loads without branches between them: they are waited for at publish()
-      const int r = rb * 256 + e;
-      const int i = min(r, v.R - 1) / p.H;
-      const bool in = r < v.R;
-      const int n = in && p.path ? p.path[(size_t)v.b * p.T + i] : i;
-      const bool ok = in && n >= 0 && n < p.T;
-      if (in && !ok && p.req_status) p.req_status[v.b] = VA_ERR_INVALID_ARG;
-      node = ok ? n : 0;
-      const size_t row = (size_t)v.b * p.T + node;
-      const uint64_t word = p.tree_mask[row * W + (node >> 6)];
-      const float l = p.lse[ok ? row * p.H + (r - i * p.H) : 0];
-      if (F8) col.x = factor * tp.q_scale[ok ? (size_t)v.b * p.T * p.H + r : 0];
-      col.y = l * kLog2e;
-      adds = ok && ((word >> (node & 63)) & 1ull) && l != -INFINITY;
-    };
-    auto publish = [&](int buf) {
-      c.col[buf][e] = col;
-      c.node[buf][e] = (uint8_t)node;
-      const uint32_t none = __ballot_sync(0xffffffffu, !adds);
-      if (lane == 0) c.inv[buf][e >> 5] = none;
-    };
     uint32_t pass = 0, tile_no = 0;
-    column(w, 0);
-    publish(0);
-    asm volatile("bar.sync 1, %0;" ::"r"(kEpiThreads) : "memory");
-    while (w.alive()) {
+    for (; w.alive(); w.next(), ++tile_no) {
       const int blocks = row_blocks(w.R);
       const int key = w.tile * kTileKeys + (int)rank * 128 + m;
       const int krow = half == 0 ? kw_pool_row(p, w.b, w.kv_len, key) : 0;
       const int P = w.kv_len - p.T;
-      const bool tail = (w.tile + 1) * kTileKeys > P;  // of the pair: warp-uniform
       // a tail key is seen by some nodes only: bit n of (seen0, seen1) for node n
+      const bool tail = w.tile * kTileKeys + (int)rank * 128 + 32 * q + 32 > P;  // of the warp
       const int nd = key - P;
       uint64_t seen0 = ~0ull, seen1 = ~0ull;
       if (tail && nd >= 0) {
@@ -516,60 +558,95 @@ kweights_tc_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_const
           if (n < 64) seen0 |= bit << n; else seen1 |= bit << (n - 64);
         }
       }
-      float sum0 = 0.f, sum1 = 0.f, sum2 = 0.f, sum3 = 0.f;
-      Walk nx = w;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
       for (int rb = 0; rb < blocks; ++rb, ++pass) {
         const int buf = pass & 1;
         const int cols = block_cols(w.R, rb) / 2;  // this half's
-        if (rb + 1 == blocks) nx.next();
-        column(nx, rb + 1 == blocks ? 0 : rb + 1);
-        warp_wait(&c.s_full[buf], (pass >> 1) & 1, abort, expired);
+        const int c0 = half * cols;
+        const uint32_t parity = (pass >> 1) & 1;
+        warp_wait(&c.i_full[buf], parity, abort, expired);
+        warp_wait(&c.s_full[buf], parity, abort, expired);
         fence_after();
-        for (int g = 0; g < cols; g += 32) {
-          const int c0 = half * cols + g;
-          float x[32];
-          ld32(tmem + lane_base + buf * 256 + c0, x);
-          wait_ld();
-          if (g + 32 == cols) {  // the scores are in registers: the buffer may be reused
-            fence_before();
-            __syncwarp();
-            if (lane == 0) arrive_cluster(free0 + buf * 8);
-          }
-          const float4* f = reinterpret_cast<const float4*>(&c.col[buf][c0]);
-          const uint32_t none = c.inv[buf][c0 >> 5];
-          if (none == 0 && !tail) {
+        const uint32_t scores = tmem + lane_base + buf * 256 + c0;
+        // one group of 32 columns: x holds its scores
+        auto group = [&](const float (&x)[32], int g) {
+          const float* l2 = &c.l2[buf][c0 + g];
+          const float* fc = &c.factor[buf][c0 + g];
+          uint32_t off = c.none[buf][(c0 + g) >> 5];  // columns that add nothing to this key
+          if (tail) {
+            const uint8_t* nodes = &c.node[buf][c0 + g];
+            const int n = c.one[buf][(c0 + g) >> 5];
+            uint32_t on = 0;
+            if (n >= 0) {  // as with 32 heads and more
+              on = ((n < 64 ? seen0 >> n : seen1 >> (n - 64)) & 1ull) ? ~0u : 0u;
+            } else {
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              const float4 a = f[i / 2], b = f[i / 2 + 1];
-              sum0 += ex2f(fmaf(x[i], a.x, -a.y));
-              sum1 += ex2f(fmaf(x[i + 1], a.z, -a.w));
-              sum2 += ex2f(fmaf(x[i + 2], b.x, -b.y));
-              sum3 += ex2f(fmaf(x[i + 3], b.z, -b.w));
+              for (int i = 0; i < 32; ++i) {
+                const int n = nodes[i];
+                on |= (uint32_t)((n < 64 ? seen0 >> n : seen1 >> (n - 64)) & 1ull) << i;
+              }
+            }
+            off |= ~on;
+          }
+          if (__any_sync(0xffffffffu, off != 0)) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float v = ex2f(fmaf(x[i], F8 ? fc[i] : factor, -l2[i]));
+              sum[i & 3] += (off >> i) & 1u ? 0.f : v;
             }
           } else {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const int n = c.node[buf][c0 + i];
-              const bool on = !((none >> i) & 1u) && (((n < 64 ? seen0 : seen1) >> (n & 63)) & 1ull);
-              const float2 a = c.col[buf][c0 + i];
-              const float v = ex2f(fmaf(x[i], a.x, -a.y));
-              sum0 += on ? v : 0.f;
+            for (int i = 0; i < 32; ++i)
+              sum[i & 3] += ex2f(fmaf(x[i], F8 ? fc[i] : factor, -l2[i]));
+          }
+        };
+        // all scores are in registers: the buffer may be written again
+        auto drained = [&]() {
+          fence_before();
+          __syncwarp();
+          if (lane == 0) arrive_cluster(free0 + buf * 8);
+        };
+        float xa[32];
+        if (F8) {  // 96 registers a thread, and bound by memory: one group at a time
+#pragma unroll 1
+          for (int g = 0; g < cols; g += 32) {
+            ld32(scores + g, xa);
+            wait_ld();
+            if (g + 32 == cols) drained();
+            group(xa, g);
+          }
+        } else {   // the next group's scores are on their way while one is worked on
+          float xb[32];
+          ld32(scores, xa);
+#pragma unroll 1
+          for (int g = 0; g < cols; g += 64) {
+            wait_ld();
+            const bool more = g + 32 < cols;
+            if (more) ld32(scores + g + 32, xb);
+            else drained();
+            group(xa, g);
+            if (more) {
+              wait_ld();
+              if (g + 64 < cols) ld32(scores + g + 64, xa);
+              else drained();
+              group(xb, g + 32);
             }
           }
         }
-        if (rb + 1 == blocks && half == 1)
-          c.xsum[tile_no & 1][m] = (sum0 + sum1) + (sum2 + sum3);
-        publish(buf ^ 1);
-        asm volatile("bar.sync 1, %0;" ::"r"(kEpiThreads) : "memory");
+        __syncwarp();
+        if (lane == 0)
+          asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&c.i_empty[buf]))
+                       : "memory");
       }
+      // the two halves of a key meet in shared memory (the quadrant's 64 threads)
+      const float s = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      if (half == 1) c.xsum[tile_no & 1][m] = s;
+      asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");
       if (half == 0 && key < w.kv_len) {
-        const float s = (sum0 + sum1) + (sum2 + sum3) + c.xsum[tile_no & 1][m];
-        kw_store(p, w.b, 0, key, krow >= 0 ? s : 0.f);
+        kw_store(p, w.b, 0, key, krow >= 0 ? s + c.xsum[tile_no & 1][m] : 0.f);
         if (krow < 0 && p.req_status) p.req_status[w.b] = VA_ERR_INVALID_ARG;
         if (*abort && p.req_status) p.req_status[w.b] = VA_ERR_CUDA;
       }
-      ++tile_no;
-      w = nx;
     }
   }
 

@@ -51,13 +51,15 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
 // and copies.  `expired` counts the waits that gave up.
 __device__ __noinline__ inline bool warp_wait_slow(uint32_t bar, uint32_t parity,
                                                    volatile int* abort, unsigned int* expired) {
-  const unsigned long long t0 = global_ns();
+  unsigned long long t0 = 0;  // read late: most waits end before the clock is needed
   for (;;) {
 #pragma unroll 1
     for (int k = 0; k < 32; ++k)
       if (__all_sync(0xffffffffu, mbar_try(bar, parity))) return true;
-    const bool give_up = __shfl_sync(
-        0xffffffffu, (*abort != 0) || (global_ns() - t0 > kTimeoutNs) ? 1 : 0, 0) != 0;
+    const unsigned long long now = global_ns();
+    if (t0 == 0) t0 = now;
+    const bool give_up =
+        __shfl_sync(0xffffffffu, (*abort != 0) || (now - t0 > kTimeoutNs) ? 1 : 0, 0) != 0;
     if (give_up) {
       if ((threadIdx.x & 31) == 0 && !*abort) {
         *abort = 1;
