@@ -7,24 +7,25 @@
 // and up to 256 rows at a time.  In tensor memory a key is then a lane and a
 // row a column, so a thread adds its key's exponentials over the columns in
 // a register, and nothing is exchanged between threads but the two halves
-// of a tile's columns.
+// of a tile's columns.  No partial sums leave the SM.
 //
-// A tile's keys (9 chunks of 64 dims, 144 KB a CTA) stay in shared memory
-// while all rows of the request pass by, so each key is read from HBM once
-// and no partial sums leave the SM.  Rows come through a ring of 16 KB slots;
-// a request of at most 128 rows has them resident instead, loaded once for
-// all of the pair's tiles.  The tiles of all requests, in order and weighted
-// by what their load and rows cost, are divided into equal contiguous
-// ranges, one per pair.
+// A request's tiles are walked in one of two layouts of shared memory.  Few rows
+// (at most 160) are loaded once per pair and request and stay, and the tiles'
+// keys come through a ring of 16 KB chunks (128 keys x 64 dims).  More rows: a
+// tile's 9 key chunks stay while the rows pass by through a ring, in equal
+// blocks.  Either way each key is read from HBM once.  The tiles of
+// all requests, in order and weighted by what they cost, are divided into
+// equal contiguous ranges, one per pair.
 //
-// FP8 cache: converter warps read the codes and write them as fp16, which
-// holds every E4M3 value; the queries are multiplied by a power of two per
-// row and stored as fp16 by a first kernel (exact down to 2^-39 of the row's
-// largest element), and the epilogue undoes it in fp32.
+// FP8 cache: the codes come through a ring of their own, and converter warps
+// write them as fp16, which holds every E4M3 value; the queries are multiplied
+// by a power of two per row and stored as fp16 by a first kernel (exact down
+// to 2^-39 of the row's largest element), and the epilogue undoes it in fp32.
 //
-// Bound by HBM for few rows (1152 or 576 bytes a key), by the operand traffic
-// from L2 into shared memory for many (64 bytes a clock and SM at the full
-// MMA rate), with the exponentials (16 a clock and SM) close behind.
+// Bound by HBM for few rows (1152 or 576 bytes a key) and by the tensor cores
+// for many (128 clocks per 256 x 256 x 16), with the latency of the rings'
+// loads close behind (about 2200 clocks from a slot's release to its refill);
+// the exponentials take 16 a clock and SM.
 #include "va_kweights.cuh"
 #include "va_tc_ops.cuh"
 
@@ -36,48 +37,54 @@ namespace {
 
 using namespace tc;
 
-constexpr int kTileKeys = 256;          // of the pair
-constexpr int kChunks = 9;              // 64-dim chunks: 8 of c_kv, 1 of k_pe
-constexpr int kKChunk = 128 * 128;      // bytes: 128 keys x 64 dims
-constexpr int kQSlots = 4;
-constexpr int kQSlot = 128 * 128;       // bytes: up to 128 rows x 64 dims
-constexpr int kQBytes = kChunks * 64 * 128;  // resident rows: 64 a CTA (>= the ring)
-constexpr int kRowsResident = 128;      // of the pair
-constexpr int kWarpK = 0, kWarpMma = 1, kWarpEpi = 2, kWarpQ = 10, kWarpInfo = 11, kWarpConv = 12;
-constexpr int kConvWarps = 8;          // 16 keys of the CTA's tile each
-constexpr int kConvAhead = 4;           // chunks whose codes are in flight
-static_assert(kQBytes >= kQSlots * kQSlot, "the ring shares the resident rows' space");
+constexpr int kTileKeys = 256;       // of the pair
+constexpr int kChunks = 9;           // 64-dim chunks of a row: 8 of c_kv, 1 of k_pe
+constexpr int kKChunk = 128 * 128;   // bytes: 128 keys x 64 dims
+constexpr int kMaxK = 12, kMaxQ = 8; // ring slots, at most
+constexpr int kRegion = kChunks * kKChunk + kChunks * 64 * 128;  // keys and rows: 216 KB
+constexpr int kRawSlots = 5, kRawSlot = 128 * 64;                // FP8 codes: 128 keys x 64 dims
+constexpr int kWarpK = 0, kWarpMma = 1, kWarpEpi = 2, kWarpQ = 10, kWarpInfo = 11, kWarpConv = 13;
+constexpr int kConvWarps = 8, kConvTeams = 4;  // a team converts every 4th chunk
 
 struct TcParams {
   KwParams k;
   int dense;             // rows of request b start at b * T * H of the q maps
-  int box_rows;          // rows of a query box
+  int run;               // rows that lie in order from a multiple of it on
   const float* q_scale;  // FP8 cache: [B, T H] power of two that undoes the row's
 };
 
+constexpr int kBoxes = 4;  // query boxes of 8, 16, 32 or 64 rows
+struct QMaps {
+  CUtensorMap nope[kBoxes], pe[kBoxes];
+};
+
 struct __align__(16) Ctl {
-  uint64_t k_full[kChunks], k_empty[kChunks];
-  uint64_t q_full[kQSlots], q_empty[kQSlots];
-  uint64_t r_full, r_empty;   // resident rows
-  uint64_t s_full[2], s_empty[2];
+  uint64_t k_full[kMaxK], k_empty[kMaxK];
+  uint64_t q_full[kMaxQ], q_empty[kMaxQ];
+  uint64_t raw_full[kRawSlots], raw_empty[kRawSlots];
+  uint64_t conv_done[kMaxK];       // FP8 cache: the slot's last conversion
+  uint64_t r_full;                 // rows that stay
+  uint64_t seg_done;               // a request's last tile of this pair is multiplied
+  uint64_t s_full[2], s_empty[2];  // scores in tensor memory
   uint64_t i_full[2], i_empty[2];  // column data of a pass
   uint64_t drain;
   long long start_off, lo, hi;
   int start_b, start_tile;
   uint32_t tmem;
   int abort;
-  // of each column of a pass: its node, its row's log2-sum and factor; and one
-  // bit where the column adds nothing (no row, absent node, empty row)
+  // of each column of a pass: its node, its row's log2-sum and factor; one bit
+  // where the column adds nothing (no row, absent node, empty row); and the
+  // node of all that a group of 32 columns adds (-1: several)
   uint32_t none[2][8];
-  int one[2][8];         // the node of all that a 32-column group adds, or -1
+  int one[2][8];
   float xsum[2][128];
   uint8_t node[2][256];
-  float l2[2][256];
-  float factor[2][256];  // FP8 cache
+  __align__(16) float l2[2][256];
+  __align__(16) float factor[2][256];  // FP8 cache
 };
 constexpr int kScanAt = offsetof(Ctl, xsum);  // the start-up scan uses xsum ..
 static_assert(kScanAt % 8 == 0, "scan alignment");
-constexpr size_t kSmemBytes = 1024 + (size_t)kChunks * kKChunk + kQBytes + sizeof(Ctl);
+constexpr size_t kSmemBytes = 1024 + kRegion + sizeof(Ctl);
 static_assert(kSmemBytes <= 232448, "shared memory of one CTA");
 
 __device__ __forceinline__ float ex2f(float x) {
@@ -86,21 +93,46 @@ __device__ __forceinline__ float ex2f(float x) {
   return y;
 }
 
-__host__ __device__ __forceinline__ int pad64(int n) { return n < 64 ? 64 : (n + 63) & ~63; }
-// Columns of row block rb of a request of R rows.
-__device__ __forceinline__ int block_cols(int R, int rb) { return pad64(min(256, R - rb * 256)); }
-__device__ __forceinline__ int row_blocks(int R) { return R <= 256 ? 1 : (R + 255) >> 8; }
-// What a tile costs: its keys' load (256) and its rows'.
-__device__ __forceinline__ int tile_cost(int R) {
-  return 256 + ((R <= 256 ? 0 : (R - 1) & ~255) + block_cols(R, row_blocks(R) - 1));
-}
+// How the rows of a request are multiplied: `blocks` passes of `cols` columns.
+// Up to kStay rows stay in shared memory: with more, fewer than 7 key chunks
+// would be in flight beside them, which HBM's latency needs (4 slots beside 256
+// rows took 8000 clocks a tile, rows through the ring 5000).  Beside an FP8
+// cache's ring of codes the key chunks only pass from the converters to the
+// tensor cores, and 4 slots do.
+template <bool F8>
+struct Shape {
+  static constexpr int kStay = F8 ? 192 : 160, kPass = F8 ? 128 : 256;
+  static constexpr int kUsable = kRegion - (F8 ? kRawSlots * kRawSlot : 0);
+  int blocks, cols;
+  bool stay;
+  __device__ __forceinline__ void set(int R) {
+    stay = R <= kStay;
+    blocks = stay ? 1 : (R + kPass - 1) / kPass;
+    cols = max(64, ((R + blocks - 1) / blocks + 63) & ~63);
+  }
+  // ring slots and where the keys and the rows lie in the region
+  __device__ __forceinline__ int k_slots() const {
+    return stay ? min(kMaxK, (kUsable - kChunks * cols * 64) / kKChunk) : kChunks;
+  }
+  __device__ __forceinline__ int k_at() const { return stay ? kChunks * cols * 64 : 0; }
+  __device__ __forceinline__ int q_slots() const {
+    return min(kMaxQ, (kUsable - kChunks * kKChunk) / (cols * 64));
+  }
+  __device__ __forceinline__ int q_at() const { return stay ? 0 : kChunks * kKChunk; }
+  // clocks of a tile: its keys' share of HBM, or 18 a column on the tensor cores
+  __device__ __forceinline__ int cost() const {
+    return max(F8 ? 3400 : 6400, blocks * (18 * cols + 500) + 500);
+  }
+};
 
 // The pair's tiles, in order.  Every warp role walks them by itself.
+template <bool F8>
 struct Walk {
   const KwParams* p;
   long long off, end;
   int b, tile, tiles, R, kv_len, cost;
   KwRequest rq;
+  Shape<F8> sh;
   __device__ __forceinline__ void load() {
     for (; b < p->B; ++b) {
       rq = kw_request(*p, b);
@@ -110,7 +142,8 @@ struct Walk {
       kv_len = rq.kv_len;
       tiles = (kv_len + kTileKeys - 1) / kTileKeys;
       R = rq.nodes * p->H;
-      cost = tile_cost(R);
+      sh.set(R);
+      cost = sh.cost();
     }
   }
   __device__ __forceinline__ void start(const KwParams& kp, const Ctl& c) {
@@ -136,35 +169,52 @@ struct Walk {
   }
 };
 
+// Position in a ring whose length changes from request to request; bit s of
+// `used` is the phase of slot s.
+struct Ring {
+  int slot = 0, n = 1;
+  uint32_t used = 0;
+  __device__ __forceinline__ void restart(int slots) { slot = 0; n = slots; }
+  __device__ __forceinline__ uint32_t phase() const { return (used >> slot) & 1u; }
+  __device__ __forceinline__ void advance() {
+    used ^= 1u << slot;
+    if (++slot == n) slot = 0;
+  }
+};
+
 template <bool F8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((kWarpConv + (F8 ? kConvWarps : 0)) * 32, 1)
-kweights_tc_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_constant__ CUtensorMap tm_qp,
-                   const __grid_constant__ CUtensorMap tm_ckv,
+kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ CUtensorMap tm_ckv,
                    const __grid_constant__ CUtensorMap tm_kpe, const __grid_constant__ TcParams tp) {
   constexpr int kThreads = (kWarpConv + (F8 ? kConvWarps : 0)) * 32;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-  uint8_t* sK = base;
-  uint8_t* sQ = sK + (size_t)kChunks * kKChunk;
-  Ctl& c = *reinterpret_cast<Ctl*>(sQ + kQBytes);
+  uint8_t* sm = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  Ctl& c = *reinterpret_cast<Ctl*>(sm + kRegion);
   const KwParams& p = tp.k;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-  unsigned int* expired = &g_kw_timeouts;
   volatile int* abort = &c.abort;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return warp_wait(bar, parity, abort, &g_kw_timeouts);
+  };
 
   if (tid == 0) {
-    for (int i = 0; i < kChunks; ++i) {
-      mbar_init(&c.k_full[i], F8 ? 2 * kConvWarps : 1);
+    for (int i = 0; i < kMaxK; ++i) {
+      mbar_init(&c.k_full[i], F8 ? 2 * (kConvWarps / kConvTeams) : 1);
       mbar_init(&c.k_empty[i], 1);
+      mbar_init(&c.conv_done[i], kConvWarps / kConvTeams);
     }
-    for (int i = 0; i < kQSlots; ++i) {
+    for (int i = 0; i < kMaxQ; ++i) {
       mbar_init(&c.q_full[i], 1);
       mbar_init(&c.q_empty[i], 1);
     }
+    for (int i = 0; i < kRawSlots; ++i) {
+      mbar_init(&c.raw_full[i], 1);
+      mbar_init(&c.raw_empty[i], kConvWarps / kConvTeams);
+    }
     mbar_init(&c.r_full, 1);
-    mbar_init(&c.r_empty, 1);
+    mbar_init(&c.seg_done, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&c.s_full[i], 1);
       mbar_init(&c.s_empty[i], 16);  // 8 epilogue warps x 2 CTAs
@@ -191,10 +241,20 @@ kweights_tc_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_const
     static_assert(sizeof(Ctl) - kScanAt >= kThreads * sizeof(long long), "scan space");
     const int q = (p.B + kThreads - 1) / kThreads;
     const int b0 = min(p.B, tid * q), b1 = min(p.B, b0 + q);
+    auto tiles_cost = [&](const KwRequest& rq, int* tiles) {
+      Shape<F8> sh;
+      sh.set(rq.nodes * p.H);
+      *tiles = (rq.kv_len + kTileKeys - 1) / kTileKeys;
+      return sh.cost();
+    };
     long long sum = 0;
     for (int b = b0; b < b1; ++b) {
       const KwRequest rq = kw_request(p, b);
-      if (rq.ok) sum += (long long)((rq.kv_len + kTileKeys - 1) / kTileKeys) * tile_cost(rq.nodes * p.H);
+      int tiles;
+      if (rq.ok) {
+        const int cost = tiles_cost(rq, &tiles);
+        sum += (long long)tiles * cost;
+      }
       if ((!rq.ok || rq.bad_accept) && blockIdx.x == 0 && p.req_status)
         p.req_status[b] = VA_ERR_INVALID_ARG;
     }
@@ -229,8 +289,8 @@ kweights_tc_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_const
       for (int b = b0; b < b1; ++b) {
         const KwRequest rq = kw_request(p, b);
         if (!rq.ok) continue;
-        const int tiles = (rq.kv_len + kTileKeys - 1) / kTileKeys;
-        const int cost = tile_cost(rq.nodes * p.H);
+        int tiles;
+        const int cost = tiles_cost(rq, &tiles);
         if (lo >= off + (long long)tiles * cost) {
           off += (long long)tiles * cost;
           continue;
@@ -249,48 +309,69 @@ kweights_tc_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_const
   cluster_sync_all();
   fence_after();
   const uint32_t tmem = c.tmem;
-  Walk w;
+  Walk<F8> w;
   w.start(p, c);
+  // Every role that touches the region begins a request's tiles alike: it waits
+  // until the pair's last request there is multiplied, for its layout goes.
+  int held = -1;
+  uint32_t seg_parity = 1;
+  auto new_request = [&](bool& go) {
+    if (held == w.b) return false;
+    held = w.b;
+    go = wait(&c.seg_done, seg_parity);
+    seg_parity ^= 1;
+    return true;
+  };
 
   if (warp == kWarpK) {
-    // ------------------------------------------------- key chunks by TMA (bf16 cache)
-    if (!F8) {
-      bool go = true;
-      uint32_t phase = 0;
-      const int oob = p.num_pages * kPage;  // past the pool: zeros
-      for (; w.alive() && go; w.next(), phase ^= 1) {
-        const int key = w.tile * kTileKeys + (int)rank * 128;
-        const int r0 = kw_pool_row(p, w.b, w.kv_len, key);
-        const int r1 = kw_pool_row(p, w.b, w.kv_len, key + kPage);
-        for (int kc = 0; kc < kChunks && go; ++kc) {
-          go = warp_wait(&c.k_empty[kc], phase ^ 1, abort, expired);
-          if (!go) break;
-          if (elect_one()) {
-            const uint32_t bar = map_to_rank(smem_u32(&c.k_full[kc]), 0);
-            if (rank == 0) arrive_expect_tx(&c.k_full[kc], 2 * kKChunk);
-            const uint32_t dst = smem_u32(sK + (size_t)kc * kKChunk);
-            const CUtensorMap* map = kc < 8 ? &tm_ckv : &tm_kpe;
-            const int x = kc < 8 ? kc * 64 : 0;
-            tma_2d(dst, map, bar, x, r0 < 0 ? oob : r0);
-            tma_2d(dst + kKChunk / 2, map, bar, x, r1 < 0 ? oob : r1);
+    // -------------------------------------------------- key chunks (or codes) by TMA
+    bool go = true;
+    Ring ring;
+    if (F8) ring.restart(kRawSlots);
+    const int oob = p.num_pages * kPage;  // past the pool: zeros
+    for (; w.alive() && go; w.next()) {
+      if (!F8 && new_request(go)) ring.restart(w.sh.k_slots());
+      const int key = w.tile * kTileKeys + (int)rank * 128;
+      int r0 = kw_pool_row(p, w.b, w.kv_len, key);
+      int r1 = kw_pool_row(p, w.b, w.kv_len, key + kPage);
+      r0 = r0 < 0 ? oob : r0;
+      r1 = r1 < 0 ? oob : r1;
+      uint8_t* ring_at = F8 ? sm + kRegion - kRawSlots * kRawSlot : sm + w.sh.k_at();
+      for (int kc = 0; kc < kChunks && go; ++kc) {
+        const int s = ring.slot;
+        go = wait(F8 ? &c.raw_empty[s] : &c.k_empty[s], ring.phase() ^ 1);
+        if (!go) break;
+        if (elect_one()) {
+          const CUtensorMap* map = kc < 8 ? &tm_ckv : &tm_kpe;
+          const int x = kc < 8 ? kc * 64 : 0;
+          if (F8) {
+            arrive_expect_tx(&c.raw_full[s], kRawSlot);
+            const uint32_t dst = smem_u32(ring_at + s * kRawSlot);
+            tma_2d_local(dst, map, &c.raw_full[s], x, r0);
+            tma_2d_local(dst + kRawSlot / 2, map, &c.raw_full[s], x, r1);
+          } else {
+            const uint32_t bar = map_to_rank(smem_u32(&c.k_full[s]), 0);
+            if (rank == 0) arrive_expect_tx(&c.k_full[s], 2 * kKChunk);
+            const uint32_t dst = smem_u32(ring_at + s * kKChunk);
+            tma_2d(dst, map, bar, x, r0);
+            tma_2d(dst + kKChunk / 2, map, bar, x, r1);
           }
-          __syncwarp();
         }
+        __syncwarp();
+        ring.advance();
       }
-      // the last use of every chunk must be over before the CTA may exit
-      for (int kc = 0; kc < kChunks && go; ++kc)
-        go = warp_wait(&c.k_empty[kc], phase ^ 1, abort, expired);
-      if (*abort) settle();
     }
+    // the last use of every slot must be over before the CTA may exit
+    for (int s = 0; s < (F8 ? kRawSlots : kMaxK) && go; ++s)
+      go = wait(F8 ? &c.raw_empty[s] : &c.k_empty[s], ((ring.used >> s) & 1u) ^ 1);
+    if (!F8 && go) wait(&c.seg_done, seg_parity);
+    if (*abort) settle();
   } else if (warp == kWarpQ) {
     // ------------------------------------------------------------ query rows by TMA
     bool go = true;
-    int slot = 0;
-    uint32_t phase = 0, rphase = 0;
-    int held = -1;           // request whose rows are resident
-    bool streaming = false;  // the space's last use was the ring
+    Ring ring;
     const long long rows_total = (long long)p.B * p.T * p.H;
-    // first map row of rows [r, r + box_rows) of the request (one node's, or dense)
+    // first map row of a box from row r of the request on
     auto map_row = [&](int r) -> int {
       if (tp.dense) return (int)((long long)w.b * p.T * p.H + r);
       if (r >= w.R) return (int)rows_total;
@@ -299,105 +380,101 @@ kweights_tc_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_const
       if (n < 0 || n >= p.T) return (int)rows_total;
       return (int)(((long long)w.b * p.T + n) * p.H + (r - i * p.H));
     };
-    auto ring_empty = [&]() {  // every slot's last rows have been used
-      for (int i = 0; i < kQSlots && go; ++i) {
-        const int s = (slot + i) % kQSlots;
-        go = warp_wait(&c.q_empty[s], (s < slot ? phase : phase ^ 1), abort, expired);
-      }
-    };
     for (; w.alive() && go; w.next()) {
-      if (w.R <= kRowsResident) {
-        if (held == w.b) continue;
-        if (streaming) ring_empty();
-        streaming = false;
-        if (go) go = warp_wait(&c.r_empty, rphase ^ 1, abort, expired);
-        if (!go) break;
-        const int half = block_cols(w.R, 0) / 2;
-        if (lane == 0 && rank == 0) arrive_expect_tx(&c.r_full, 2 * half * 128 * kChunks);
-        __syncwarp();
-        const uint32_t bar = map_to_rank(smem_u32(&c.r_full), 0);
-        if (lane < half / tp.box_rows) {
-          const int y = map_row((int)rank * half + lane * tp.box_rows);
-          for (int kc = 0; kc < kChunks; ++kc)
-            tma_2d(smem_u32(sQ + kc * half * 128 + lane * tp.box_rows * 128),
-                   kc < 8 ? &tm_qn : &tm_qp, bar, kc < 8 ? kc * 64 : 0, y);
+      const bool fresh = new_request(go);
+      if (!go || (!fresh && w.sh.stay)) continue;
+      if (fresh) ring.restart(!w.sh.stay ? w.sh.q_slots() : 1);
+      const int half = w.sh.cols / 2, bytes = half * 128;
+      int box = kBoxes - 1;  // the tallest box that fits the half and the run
+      while (box > 0 && ((half | tp.run) & ((8 << box) - 1))) --box;
+      const int box_rows = 8 << box;
+      const CUtensorMap* tm_qn = &tm_q.nope[box];
+      const CUtensorMap* tm_qp = &tm_q.pe[box];
+      const bool mine = lane < half / box_rows;
+      uint8_t* at = sm + w.sh.q_at() + lane * box_rows * 128;
+      for (int rb = 0; rb < w.sh.blocks && go; ++rb) {
+        const int y = mine ? map_row(rb * w.sh.cols + (int)rank * half + lane * box_rows) : 0;
+        if (w.sh.stay) {  // all nine chunks at once, to stay
+          if (lane == 0 && rank == 0) arrive_expect_tx(&c.r_full, 2 * bytes * kChunks);
+          __syncwarp();
+          const uint32_t bar = map_to_rank(smem_u32(&c.r_full), 0);
+          if (mine)
+            for (int kc = 0; kc < kChunks; ++kc)
+              tma_2d(smem_u32(at + kc * bytes), kc < 8 ? tm_qn : tm_qp, bar, kc < 8 ? kc * 64 : 0, y);
+          __syncwarp();
+          continue;
         }
-        __syncwarp();
-        rphase ^= 1;
-        held = w.b;
-      } else {
-        if (held >= 0) {  // resident rows of the last request: wait for their last use
-          go = warp_wait(&c.r_empty, rphase ^ 1, abort, expired);
-          held = -1;
-        }
-        streaming = true;
-        const int blocks = row_blocks(w.R);
-        for (int rb = 0; rb < blocks && go; ++rb) {
-          const int half = block_cols(w.R, rb) / 2;
-          const bool mine = lane < half / tp.box_rows;
-          const int y = mine ? map_row(rb * 256 + (int)rank * half + lane * tp.box_rows) : 0;
-          for (int kc = 0; kc < kChunks && go; ++kc) {
-            go = warp_wait(&c.q_empty[slot], phase ^ 1, abort, expired);
-            if (!go) break;
-            if (lane == 0 && rank == 0) arrive_expect_tx(&c.q_full[slot], 2 * half * 128);
-            __syncwarp();
-            if (mine)
-              tma_2d(smem_u32(sQ + slot * kQSlot + lane * tp.box_rows * 128),
-                     kc < 8 ? &tm_qn : &tm_qp, map_to_rank(smem_u32(&c.q_full[slot]), 0),
-                     kc < 8 ? kc * 64 : 0, y);
-            __syncwarp();
-            if (++slot == kQSlots) { slot = 0; phase ^= 1; }
-          }
+        for (int kc = 0; kc < kChunks && go; ++kc) {
+          const int s = ring.slot;
+          go = wait(&c.q_empty[s], ring.phase() ^ 1);
+          if (!go) break;
+          if (lane == 0 && rank == 0) arrive_expect_tx(&c.q_full[s], 2 * bytes);
+          __syncwarp();
+          if (mine)
+            tma_2d(smem_u32(at + s * bytes), kc < 8 ? tm_qn : tm_qp,
+                   map_to_rank(smem_u32(&c.q_full[s]), 0), kc < 8 ? kc * 64 : 0, y);
+          __syncwarp();
+          ring.advance();
         }
       }
     }
-    if (go) ring_empty();
-    if (go) warp_wait(&c.r_empty, rphase ^ 1, abort, expired);
+    for (int s = 0; s < kMaxQ && go; ++s) go = wait(&c.q_empty[s], ((ring.used >> s) & 1u) ^ 1);
+    if (go) wait(&c.seg_done, seg_parity);
     if (*abort) settle();
   } else if (warp == kWarpMma) {
     // ------------------------------------------------------------------ MMA issue
     if (rank == 0) {
       bool ok = true;
-      int slot = 0, held = -1;
-      uint32_t qphase = 0, kphase = 0, rphase = 0, pass = 0;
-      const uint64_t dk = sw128_desc(smem_u32(sK)), dq = sw128_desc(smem_u32(sQ));
-      for (; w.alive() && ok; w.next(), kphase ^= 1) {
-        const bool resident = w.R <= kRowsResident;
-        if (resident && held != w.b) {
-          ok = warp_wait(&c.r_full, rphase, abort, expired);
-          rphase ^= 1;
+      Ring kring, qring;
+      uint32_t rphase = 0, pass = 0;
+      const uint64_t desc = sw128_desc(smem_u32(sm));
+      for (; w.alive() && ok; w.next()) {
+        const bool stream = !w.sh.stay;
+        const int bytes = w.sh.cols * 64;  // of a chunk of this CTA's rows
+        if (held != w.b) {
           held = w.b;
+          kring.restart(w.sh.k_slots());
+          qring.restart(stream ? w.sh.q_slots() : 1);
+          if (!stream) {
+            ok = wait(&c.r_full, rphase);
+            rphase ^= 1;
+          }
         }
-        if (!resident) held = -1;
-        const int blocks = row_blocks(w.R);
-        for (int rb = 0; rb < blocks && ok; ++rb, ++pass) {
-          const int cols = block_cols(w.R, rb);
-          // kind::f16: fp32 sums; A, B bf16 (1) or fp16 (0), K-major; M = 256
-          const uint32_t idesc = (1u << 4) | (F8 ? 0u : (1u << 7) | (1u << 10)) |
-                                 ((uint32_t)(cols >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
+        // kind::f16: fp32 sums; A, B bf16 (1) or fp16 (0), K-major; M = 256
+        const uint32_t idesc = (1u << 4) | (F8 ? 0u : (1u << 7) | (1u << 10)) |
+                               ((uint32_t)(w.sh.cols >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
+        const uint64_t dk = desc + (uint64_t)(w.sh.k_at() >> 4);
+        const uint64_t dq = desc + (uint64_t)(w.sh.q_at() >> 4);
+        const bool seg_end = w.last_of_request();
+        const Ring first = kring;  // the tile's first chunk: every block begins there
+        for (int rb = 0; rb < w.sh.blocks && ok; ++rb, ++pass) {
           const uint32_t d = tmem + (pass & 1) * 256;
-          ok = warp_wait(&c.s_empty[pass & 1], ((pass >> 1) & 1) ^ 1, abort, expired);
+          const bool last = rb == w.sh.blocks - 1;
+          if (rb > 0) kring = first;
+          ok = wait(&c.s_empty[pass & 1], ((pass >> 1) & 1) ^ 1);
           for (int kc = 0; kc < kChunks && ok; ++kc) {
-            if (rb == 0) ok = warp_wait(&c.k_full[kc], kphase, abort, expired);
-            if (ok && !resident) ok = warp_wait(&c.q_full[slot], qphase, abort, expired);
+            const int ks = kring.slot, qs = qring.slot;
+            if (rb == 0) ok = wait(&c.k_full[ks], kring.phase());
+            if (ok && stream) ok = wait(&c.q_full[qs], qring.phase());
             if (!ok) break;
             if (elect_one()) {
               fence_after();
-              const uint64_t a = dk + (uint64_t)((kc * kKChunk) >> 4);
-              const uint64_t b = dq + (uint64_t)((resident ? kc * cols * 64 : slot * kQSlot) >> 4);
+              const uint64_t a = dk + (uint64_t)((ks * kKChunk) >> 4);
+              const uint64_t b = dq + (uint64_t)(((stream ? qs : kc) * bytes) >> 4);
               mma_pair(d, a, b, idesc, kc != 0);
               mma_pair(d, a + 2, b + 2, idesc, 1u);
               mma_pair(d, a + 4, b + 4, idesc, 1u);
               mma_pair(d, a + 6, b + 6, idesc, 1u);
-              if (!resident) commit_pair(&c.q_empty[slot]);
-              if (rb == blocks - 1) commit_pair(&c.k_empty[kc]);
+              if (stream) commit_pair(&c.q_empty[qs]);
+              if (last) commit_pair(&c.k_empty[ks]);
               if (kc == kChunks - 1) {
                 commit_pair(&c.s_full[pass & 1]);
-                if (resident && w.last_of_request()) commit_pair(&c.r_empty);
+                if (last && seg_end) commit_pair(&c.seg_done);
               }
             }
             __syncwarp();
-            if (!resident && ++slot == kQSlots) { slot = 0; qphase ^= 1; }
+            kring.advance();
+            if (stream) qring.advance();
           }
         }
       }
@@ -408,126 +485,119 @@ kweights_tc_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_const
       }
     }
   } else if (F8 && warp >= kWarpConv) {
-    // ------------------------------------------- key chunks from FP8 codes, as fp16
-    // A warp converts 16 keys of one page.  Of a chunk, lane l reads 16 codes (l & 3)
-    // of keys l / 4 + 8 i, so that 4 lanes read a key's 64 bytes; the codes of the
-    // next kConvAhead chunks are in flight in registers (volatile: loads stay there).
-    const int m0 = (warp - kWarpConv) * 16, sub = lane >> 2, u0 = lane & 3;
-    const uint8_t* ckv = reinterpret_cast<const uint8_t*>(p.c_kv) + u0 * 16;
-    const uint8_t* kpe = reinterpret_cast<const uint8_t*>(p.k_pe) + u0 * 16;
-    uint4 code[kChunks][2];
-    // pool row of the warp's first key, and how many of its keys exist
-    struct Keys { int row, n; };
-    auto keys_of = [&](const Walk& v) {
-      Keys k{0, 0};
-      if (!v.alive()) return k;
-      const int key = v.tile * kTileKeys + (int)rank * 128 + m0;
-      const int row = kw_pool_row(p, v.b, v.kv_len, key);
-      if (row >= 0) { k.row = row; k.n = v.kv_len - key; }
-      return k;
-    };
-    auto fetch = [&](int kc, const Keys& k) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        uint4& v = code[kc][i];
-        v = make_uint4(0, 0, 0, 0);
-        const int r = sub + 8 * i;
-        const uint8_t* src = kc < 8 ? ckv + (size_t)(k.row + r) * kDc + kc * 64
-                                    : kpe + (size_t)(k.row + r) * kDr;
-        if (r < k.n)
-          asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(src));
-      }
-    };
+    // ------------------------------------------------------- FP8 codes to fp16 chunks
+    // The teams work on different chunks at once, because a chunk's path (code wait,
+    // loads, conversion, stores, proxy fence, arrival) takes over 1000 clocks.  Two
+    // warps a team, 64 keys each: lane l has codes 16 (l & 3) .. of keys l / 4 + 8 i.
+    // A phase bit cannot tell a slot's last use from the one two before, and another
+    // team may still be at the last one: a team waits until that one is converted
+    // (conv_done) before it asks whether it is multiplied.  conv_done itself cannot be
+    // two behind: a chunk's codes arrive only when the chunks 5 and more before it
+    // have been read, so that their teams are done with the chunks 9 and more before,
+    // and two rounds of a ring are at least 10 chunks, or 8 of this team's own ring
+    // of 4; a new layout waits for all.
+    constexpr int kKeysPerWarp = 128 * kConvTeams / kConvWarps;
+    const int cw = warp - kWarpConv, team = cw % kConvTeams;
+    const int m0 = cw / kConvTeams * kKeysPerWarp, sub = lane >> 2, u0 = lane & 3;
     const uint32_t full0 = map_to_rank(smem_u32(&c.k_full[0]), 0);
-    Keys keys = keys_of(w);
-#pragma unroll
-    for (int kc = 0; kc < kConvAhead; ++kc) fetch(kc, keys);
-    uint32_t phase = 0;
+    const uint8_t* codes = sm + kRegion - kRawSlots * kRawSlot + (m0 + sub) * 64 + u0 * 16;
     bool go = true;
-    while (w.alive() && go) {
-      w.next();
-      const Keys next = keys_of(w);
+    Ring raw, ring;
+    raw.restart(kRawSlots);
+    int turn = 0;
+    for (; w.alive() && go; w.next()) {
+      if (new_request(go)) ring.restart(w.sh.k_slots());
+      uint8_t* k_at = sm + w.sh.k_at() + (m0 + sub) * 128;
+      for (int kc = 0; kc < kChunks && go; ++kc) {
+        if (turn == team) {
+          go = wait(&c.raw_full[raw.slot], raw.phase());
+          if (go) go = wait(&c.conv_done[ring.slot], ring.phase() ^ 1);
+          if (go) go = wait(&c.k_empty[ring.slot], ring.phase() ^ 1);
+          if (!go) break;
+#pragma unroll 2
+          for (int i = 0; i < kKeysPerWarp / 8; ++i) {
+            const uint4 v = *reinterpret_cast<const uint4*>(codes + raw.slot * kRawSlot + i * 512);
+            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+            uint32_t o[8];
 #pragma unroll
-      for (int kc = 0; kc < kChunks; ++kc) {
-        if (kc + kConvAhead < kChunks) fetch(kc + kConvAhead, keys);
-        else fetch(kc + kConvAhead - kChunks, next);
-        if (go) go = warp_wait(&c.k_empty[kc], phase ^ 1, abort, expired);
-        uint8_t* dst = sK + (size_t)kc * kKChunk + m0 * 128;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int r = sub + 8 * i;
-          const uint32_t cw[4] = {code[kc][i].x, code[kc][i].y, code[kc][i].z, code[kc][i].w};
-          uint32_t o[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const __half2_raw f = __nv_cvt_fp8x2_to_halfraw2(
-                (__nv_fp8x2_storage_t)(cw[j >> 1] >> (16 * (j & 1))), __NV_E4M3);
-            o[j] = (uint32_t)f.x | (uint32_t)f.y << 16;
+            for (int j = 0; j < 8; ++j) {
+              const __half2_raw f = __nv_cvt_fp8x2_to_halfraw2(
+                  (__nv_fp8x2_storage_t)(x[j >> 1] >> (16 * (j & 1))), __NV_E4M3);
+              o[j] = (uint32_t)f.x | (uint32_t)f.y << 16;
+            }
+            uint8_t* to = k_at + ring.slot * kKChunk + i * 1024;  // key m0 + sub + 8 i
+            *reinterpret_cast<uint4*>(to + (((2 * u0) ^ sub) << 4)) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4*>(to + (((2 * u0 + 1) ^ sub) << 4)) =
+                make_uint4(o[4], o[5], o[6], o[7]);
           }
-          uint8_t* row = dst + r * 128;
-          *reinterpret_cast<uint4*>(row + (((2 * u0) ^ (r & 7)) << 4)) =
-              make_uint4(o[0], o[1], o[2], o[3]);
-          *reinterpret_cast<uint4*>(row + (((2 * u0 + 1) ^ (r & 7)) << 4)) =
-              make_uint4(o[4], o[5], o[6], o[7]);
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) {
+            arrive(&c.raw_empty[raw.slot]);
+            arrive(&c.conv_done[ring.slot]);
+            arrive_cluster(full0 + ring.slot * 8);
+          }
         }
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) arrive_cluster(full0 + kc * 8);
+        turn = turn + 1 == kConvTeams ? 0 : turn + 1;
+        raw.advance();
+        ring.advance();
       }
-      keys = next;
-      phase ^= 1;
     }
-    for (int kc = 0; kc < kChunks && go; ++kc)
-      go = warp_wait(&c.k_empty[kc], phase ^ 1, abort, expired);
-  } else if (warp == kWarpInfo) {
+    for (int s = 0; s < kMaxK && go; ++s) go = wait(&c.k_empty[s], ((ring.used >> s) & 1u) ^ 1);
+    if (go) wait(&c.seg_done, seg_parity);
+  } else if (warp == kWarpInfo || warp == kWarpInfo + 1) {
     // ------------------------------------------------------- column data of each pass
-    // One pass ahead of the epilogue, so that its loads are off the epilogue's path.
+    // Ahead of the epilogue, so that their loads are off its path: one warp for each
+    // buffer, that is for every second pass.
     const int W = (p.T + 63) >> 6;
     uint32_t pass = 0;
     bool go = true;
     for (; w.alive() && go; w.next()) {
-      const int blocks = row_blocks(w.R);
-      for (int rb = 0; rb < blocks && go; ++rb, ++pass) {
+      for (int rb = 0; rb < w.sh.blocks && go; ++rb, ++pass) {
         const int buf = pass & 1;
-        float l[8], f[8];
-        uint64_t word[8];
-        int node[8];
-        bool ok[8];
+        if (buf != warp - kWarpInfo) continue;
+        bool free = false;
+#pragma unroll 1
+        for (int k0 = 0; k0 * 32 < w.sh.cols && go; k0 += 4) {
+          float l[4], f[4];
+          uint64_t word[4];
+          int node[4];
+          bool ok[4];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const int r = rb * 256 + k * 32 + lane;
-          const bool in = r < w.R;
-          const int i = in ? r / p.H : 0;
-          const int n = in && p.path ? p.path[(size_t)w.b * p.T + i] : i;
-          ok[k] = in && n >= 0 && n < p.T;
-          if (in && !ok[k] && p.req_status) p.req_status[w.b] = VA_ERR_INVALID_ARG;
-          node[k] = ok[k] ? n : 0;
-          const size_t row = (size_t)w.b * p.T + node[k];
-          word[k] = p.tree_mask[row * W + (node[k] >> 6)];
-          l[k] = p.lse[ok[k] ? row * p.H + (r - i * p.H) : 0];
-          f[k] = F8 && ok[k] ? tp.q_scale[(size_t)w.b * p.T * p.H + r] : 0.f;
-        }
-        go = warp_wait(&c.i_empty[buf], ((pass >> 1) & 1) ^ 1, abort, expired);
+          for (int k = 0; k < 4; ++k) {
+            const int e = (k0 + k) * 32 + lane, r = rb * w.sh.cols + e;
+            const bool in = r < w.R && e < w.sh.cols;
+            const int i = in ? r / p.H : 0;
+            const int n = in && p.path ? p.path[(size_t)w.b * p.T + i] : i;
+            ok[k] = in && n >= 0 && n < p.T;
+            if (in && !ok[k] && p.req_status) p.req_status[w.b] = VA_ERR_INVALID_ARG;
+            node[k] = ok[k] ? n : 0;
+            const size_t row = (size_t)w.b * p.T + node[k];
+            word[k] = p.tree_mask[row * W + (node[k] >> 6)];
+            l[k] = p.lse[ok[k] ? row * p.H + (r - i * p.H) : 0];
+            f[k] = F8 && ok[k] ? tp.q_scale[(size_t)w.b * p.T * p.H + r] : 0.f;
+          }
+          if (!free) go = wait(&c.i_empty[buf], ((pass >> 1) & 1) ^ 1);
+          free = true;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const bool adds = ok[k] && ((word[k] >> (node[k] & 63)) & 1ull) && l[k] != -INFINITY;
-          const int e = k * 32 + lane;
-          c.node[buf][e] = (uint8_t)node[k];
-          c.l2[buf][e] = l[k] * kLog2e;
-          if (F8) c.factor[buf][e] = adds ? f[k] * (p.scale * kLog2e) : 0.f;
-          const uint32_t none = __ballot_sync(0xffffffffu, !adds);
-          const int first = __shfl_sync(0xffffffffu, node[k], none == ~0u ? 0 : __ffs(~none) - 1);
-          const bool same = __all_sync(0xffffffffu, !adds || node[k] == first);
-          if (lane == 0) {
-            c.none[buf][k] = none;
-            c.one[buf][k] = same ? first : -1;
+          for (int k = 0; k < 4; ++k) {
+            const bool adds = ok[k] && ((word[k] >> (node[k] & 63)) & 1ull) && l[k] != -INFINITY;
+            const int e = (k0 + k) * 32 + lane;
+            c.node[buf][e] = (uint8_t)node[k];
+            c.l2[buf][e] = l[k] * kLog2e;
+            if (F8) c.factor[buf][e] = adds ? f[k] * (p.scale * kLog2e) : 0.f;
+            const uint32_t on = __ballot_sync(0xffffffffu, adds);
+            const int first = __shfl_sync(0xffffffffu, node[k], on ? __ffs(on) - 1 : 0);
+            const bool same = __all_sync(0xffffffffu, !adds || node[k] == first);
+            if (lane == 0) {
+              c.none[buf][k0 + k] = ~on;
+              c.one[buf][k0 + k] = same ? first : -1;
+            }
           }
         }
         __syncwarp();
-        if (lane == 0)
-          asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&c.i_full[buf]))
-                       : "memory");
+        if (lane == 0) arrive(&c.i_full[buf]);
       }
     }
   } else if (warp >= kWarpEpi && warp < kWarpQ) {
@@ -541,9 +611,10 @@ kweights_tc_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_const
     const int W = (p.T + 63) >> 6;
     uint32_t pass = 0, tile_no = 0;
     for (; w.alive(); w.next(), ++tile_no) {
-      const int blocks = row_blocks(w.R);
       const int key = w.tile * kTileKeys + (int)rank * 128 + m;
       const int krow = half == 0 ? kw_pool_row(p, w.b, w.kv_len, key) : 0;
+      const size_t slot = (size_t)w.b * p.max_pages * kPage + key;
+      const float old = half == 0 && p.weights_in && key < w.kv_len ? p.weights_in[slot] : 0.f;
       const int P = w.kv_len - p.T;
       // a tail key is seen by some nodes only: bit n of (seen0, seen1) for node n
       const bool tail = w.tile * kTileKeys + (int)rank * 128 + 32 * q + 32 > P;  // of the warp
@@ -558,36 +629,44 @@ kweights_tc_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_const
           if (n < 64) seen0 |= bit << n; else seen1 |= bit << (n - 64);
         }
       }
+      auto sees = [&](int n) -> uint32_t {
+        return (uint32_t)((n < 64 ? seen0 >> n : seen1 >> (n - 64)) & 1ull);
+      };
+      const int cols = w.sh.cols / 2, c0 = half * cols;  // this half's: a multiple of 32
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int rb = 0; rb < blocks; ++rb, ++pass) {
+      for (int rb = 0; rb < w.sh.blocks; ++rb, ++pass) {
         const int buf = pass & 1;
-        const int cols = block_cols(w.R, rb) / 2;  // this half's
-        const int c0 = half * cols;
         const uint32_t parity = (pass >> 1) & 1;
-        warp_wait(&c.i_full[buf], parity, abort, expired);
-        warp_wait(&c.s_full[buf], parity, abort, expired);
+        wait(&c.i_full[buf], parity);
+        wait(&c.s_full[buf], parity);
         fence_after();
         const uint32_t scores = tmem + lane_base + buf * 256 + c0;
-        // one group of 32 columns: x holds its scores
-        auto group = [&](const float (&x)[32], int g) {
-          const float* l2 = &c.l2[buf][c0 + g];
-          const float* fc = &c.factor[buf][c0 + g];
-          uint32_t off = c.none[buf][(c0 + g) >> 5];  // columns that add nothing to this key
-          if (tail) {
-            const uint8_t* nodes = &c.node[buf][c0 + g];
-            const int n = c.one[buf][(c0 + g) >> 5];
-            uint32_t on = 0;
-            if (n >= 0) {  // as with 32 heads and more
-              on = ((n < 64 ? seen0 >> n : seen1 >> (n - 64)) & 1ull) ? ~0u : 0u;
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const int n = nodes[i];
-                on |= (uint32_t)((n < 64 ? seen0 >> n : seen1 >> (n - 64)) & 1ull) << i;
-              }
-            }
-            off |= ~on;
+        // One body for all groups, and small: the roles' loops share the instruction
+        // cache, and with three unrolled copies of this one a quarter of all stalls
+        // were waits for instructions.
+#pragma unroll 1
+        for (int g = 0; g < cols; g += 32) {
+          float x[32];
+          ld32(scores + g, x);
+          wait_ld();
+          if (g + 32 == cols) {  // all scores are in registers: the buffer may be written again
+            fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_cluster(free0 + buf * 8);
           }
+          const int at = c0 + g;
+          uint32_t off = c.none[buf][at >> 5];  // columns that add nothing to this key
+          if (tail) {
+            const int n = c.one[buf][at >> 5];
+            if (n >= 0) {  // as with 32 heads and more
+              if (!sees(n)) off = ~0u;
+            } else {
+#pragma unroll 1
+              for (int i = 0; i < 32; ++i) off |= (sees(c.node[buf][at + i]) ^ 1u) << i;
+            }
+          }
+          const float* l2 = &c.l2[buf][at];
+          const float* fc = &c.factor[buf][at];
           if (__any_sync(0xffffffffu, off != 0)) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
@@ -599,51 +678,16 @@ kweights_tc_kernel(const __grid_constant__ CUtensorMap tm_qn, const __grid_const
             for (int i = 0; i < 32; ++i)
               sum[i & 3] += ex2f(fmaf(x[i], F8 ? fc[i] : factor, -l2[i]));
           }
-        };
-        // all scores are in registers: the buffer may be written again
-        auto drained = [&]() {
-          fence_before();
-          __syncwarp();
-          if (lane == 0) arrive_cluster(free0 + buf * 8);
-        };
-        float xa[32];
-        if (F8) {  // 96 registers a thread, and bound by memory: one group at a time
-#pragma unroll 1
-          for (int g = 0; g < cols; g += 32) {
-            ld32(scores + g, xa);
-            wait_ld();
-            if (g + 32 == cols) drained();
-            group(xa, g);
-          }
-        } else {   // the next group's scores are on their way while one is worked on
-          float xb[32];
-          ld32(scores, xa);
-#pragma unroll 1
-          for (int g = 0; g < cols; g += 64) {
-            wait_ld();
-            const bool more = g + 32 < cols;
-            if (more) ld32(scores + g + 32, xb);
-            else drained();
-            group(xa, g);
-            if (more) {
-              wait_ld();
-              if (g + 64 < cols) ld32(scores + g + 64, xa);
-              else drained();
-              group(xb, g + 32);
-            }
-          }
         }
         __syncwarp();
-        if (lane == 0)
-          asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&c.i_empty[buf]))
-                       : "memory");
+        if (lane == 0) arrive(&c.i_empty[buf]);
       }
       // the two halves of a key meet in shared memory (the quadrant's 64 threads)
       const float s = (sum[0] + sum[1]) + (sum[2] + sum[3]);
       if (half == 1) c.xsum[tile_no & 1][m] = s;
       asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");
       if (half == 0 && key < w.kv_len) {
-        kw_store(p, w.b, 0, key, krow >= 0 ? s + c.xsum[tile_no & 1][m] : 0.f);
+        p.weights[slot] = p.decay * old + (krow >= 0 ? s + c.xsum[tile_no & 1][m] : 0.f);
         if (krow < 0 && p.req_status) p.req_status[w.b] = VA_ERR_INVALID_ARG;
         if (*abort && p.req_status) p.req_status[w.b] = VA_ERR_CUDA;
       }
@@ -744,7 +788,7 @@ cudaError_t launch_kweights_tc(const va_key_weight_args& a, const KwParams& p, i
   TcParams tp;
   tp.k = p;
   tp.dense = needs_rows(a);
-  tp.box_rows = tp.dense || !a.path || a.H % 32 == 0 ? 32 : a.H % 16 == 0 ? 16 : 8;
+  tp.run = tp.dense || !a.path ? 64 : a.H;
   tp.q_scale = nullptr;
   const void* qn = a.q_nope;
   const void* qp = a.q_pe;
@@ -761,24 +805,23 @@ cudaError_t launch_kweights_tc(const va_key_weight_args& a, const KwParams& p, i
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  CUtensorMap tqn, tqp, tckv, tkpe;
-  if (!encode_rows(&tqn, qn, rows, kDc, tp.box_rows, f8) ||
-      !encode_rows(&tqp, qp, rows, kDr, tp.box_rows, f8))
+  QMaps tq;
+  CUtensorMap tckv, tkpe;
+  const uint64_t pool = (uint64_t)a.num_pages * kPage;
+  for (int i = 0; i < kBoxes; ++i)
+    if (!encode_rows(&tq.nope[i], qn, rows, kDc, 8 << i, f8 ? Elem::f16 : Elem::bf16) ||
+        !encode_rows(&tq.pe[i], qp, rows, kDr, 8 << i, f8 ? Elem::f16 : Elem::bf16))
+      return cudaErrorInvalidValue;
+  if (!encode_rows(&tckv, a.c_kv, pool, kDc, kPage, f8 ? Elem::u8 : Elem::bf16) ||
+      !encode_rows(&tkpe, a.k_pe, pool, kDr, kPage, f8 ? Elem::u8 : Elem::bf16))
     return cudaErrorInvalidValue;
-  if (f8) {  // the converters read the cache: no maps over it
-    tckv = tqn;
-    tkpe = tqp;
-  } else if (!encode_rows(&tckv, a.c_kv, (uint64_t)a.num_pages * kPage, kDc, kPage, false) ||
-             !encode_rows(&tkpe, a.k_pe, (uint64_t)a.num_pages * kPage, kDr, kPage, false)) {
-    return cudaErrorInvalidValue;
-  }
   const long long tiles = (long long)a.B * (((long long)a.max_pages * kPage + kTileKeys - 1) / kTileKeys);
   const int pairs = (int)(tiles < sms / 2 ? tiles : sms / 2);
   auto* k = f8 ? kweights_tc_kernel<true> : kweights_tc_kernel<false>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
   if (e != cudaSuccess) return e;
   const int threads = (kWarpConv + (f8 ? kConvWarps : 0)) * 32;
-  k<<<2 * pairs, threads, kSmemBytes, st>>>(tqn, tqp, tckv, tkpe, tp);
+  k<<<2 * pairs, threads, kSmemBytes, st>>>(tq, tckv, tkpe, tp);
   return cudaGetLastError();
 }
 
