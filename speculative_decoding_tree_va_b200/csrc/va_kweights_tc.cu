@@ -40,11 +40,16 @@ using namespace tc;
 constexpr int kTileKeys = 256;       // of the pair
 constexpr int kChunks = 9;           // 64-dim chunks of a row: 8 of c_kv, 1 of k_pe
 constexpr int kKChunk = 128 * 128;   // bytes: 128 keys x 64 dims
-constexpr int kMaxK = 12, kMaxQ = 8; // ring slots, at most
+constexpr int kMaxK = 12, kMaxQ = 8; // ring slots, at most (codes: kMaxRaw = kMaxK)
 constexpr int kRegion = kChunks * kKChunk + kChunks * 64 * 128;  // keys and rows: 216 KB
-constexpr int kRawSlots = 5, kRawSlot = 128 * 64;                // FP8 codes: 128 keys x 64 dims
-constexpr int kWarpK = 0, kWarpMma = 1, kWarpEpi = 2, kWarpQ = 10, kWarpInfo = 11, kWarpConv = 13;
+constexpr int kMaxRaw = 12, kRawSlot = 128 * 64;  // FP8 codes: 128 keys x 64 dims
+constexpr int kWarpK = 0, kWarpMma = 1, kWarpEpi = 2, kWarpQ = 10, kWarpInfo = 11;
 constexpr int kConvWarps = 8, kConvTeams = 4;  // a team converts every 4th chunk
+// Warps of column data: two for a bf16 cache, whose passes may be short; with an
+// FP8 cache one, which leaves 96 registers a thread beside the converters.
+template <bool F8> constexpr int kInfoWarps = F8 ? 1 : 2;
+template <bool F8> constexpr int kWarpConv = kWarpInfo + kInfoWarps<F8>;
+template <bool F8> constexpr int kWarps = kWarpConv<F8> + (F8 ? kConvWarps : 0);
 
 struct TcParams {
   KwParams k;
@@ -61,8 +66,7 @@ struct QMaps {
 struct __align__(16) Ctl {
   uint64_t k_full[kMaxK], k_empty[kMaxK];
   uint64_t q_full[kMaxQ], q_empty[kMaxQ];
-  uint64_t raw_full[kRawSlots], raw_empty[kRawSlots];
-  uint64_t conv_done[kMaxK];       // FP8 cache: the slot's last conversion
+  uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];
   uint64_t r_full;                 // rows that stay
   uint64_t seg_done;               // a request's last tile of this pair is multiplied
   uint64_t s_full[2], s_empty[2];  // scores in tensor memory
@@ -96,13 +100,13 @@ __device__ __forceinline__ float ex2f(float x) {
 // How the rows of a request are multiplied: `blocks` passes of `cols` columns.
 // Up to kStay rows stay in shared memory: with more, fewer than 7 key chunks
 // would be in flight beside them, which HBM's latency needs (4 slots beside 256
-// rows took 8000 clocks a tile, rows through the ring 5000).  Beside an FP8
-// cache's ring of codes the key chunks only pass from the converters to the
-// tensor cores, and 4 slots do.
+// rows took 8000 clocks a tile, rows through the ring 5000).  With an FP8 cache
+// it is the codes that HBM's latency holds up: their ring gets the room, and 4
+// slots do for the key chunks on their way from the converters.
 template <bool F8>
 struct Shape {
   static constexpr int kStay = F8 ? 192 : 160, kPass = F8 ? 128 : 256;
-  static constexpr int kUsable = kRegion - (F8 ? kRawSlots * kRawSlot : 0);
+  static constexpr int kConvRing = 4 * kKChunk, kRawBeside = 5;
   int blocks, cols;
   bool stay;
   __device__ __forceinline__ void set(int R) {
@@ -110,18 +114,26 @@ struct Shape {
     blocks = stay ? 1 : (R + kPass - 1) / kPass;
     cols = max(64, ((R + blocks - 1) / blocks + 63) & ~63);
   }
-  // ring slots and where the keys and the rows lie in the region
+  // ring slots, and where keys, rows and codes lie in the region
+  __device__ __forceinline__ int rows_stay() const { return kChunks * cols * 64; }
   __device__ __forceinline__ int k_slots() const {
-    return stay ? min(kMaxK, (kUsable - kChunks * cols * 64) / kKChunk) : kChunks;
+    return !stay ? kChunks : F8 ? 4 : min(kMaxK, (kRegion - rows_stay()) / kKChunk);
   }
-  __device__ __forceinline__ int k_at() const { return stay ? kChunks * cols * 64 : 0; }
+  __device__ __forceinline__ int k_at() const { return stay ? rows_stay() : 0; }
   __device__ __forceinline__ int q_slots() const {
-    return min(kMaxQ, (kUsable - kChunks * kKChunk) / (cols * 64));
+    return min(kMaxQ, (kRegion - kChunks * kKChunk - (F8 ? kRawBeside * kRawSlot : 0)) / (cols * 64));
   }
   __device__ __forceinline__ int q_at() const { return stay ? 0 : kChunks * kKChunk; }
-  // clocks of a tile: its keys' share of HBM, or 18 a column on the tensor cores
+  __device__ __forceinline__ int raw_slots() const {
+    return stay ? min(kMaxRaw, (kRegion - rows_stay() - kConvRing) / kRawSlot) : kRawBeside;
+  }
+  __device__ __forceinline__ int raw_at() const {
+    return stay ? rows_stay() + kConvRing : kRegion - kRawBeside * kRawSlot;
+  }
+  // Clocks of a tile, as measured: few rows wait for the keys' share of HBM, rows
+  // through the ring for its latency (5400 a pass of 192 columns, 6500 of 256).
   __device__ __forceinline__ int cost() const {
-    return max(F8 ? 3400 : 6400, blocks * (18 * cols + 500) + 500);
+    return stay ? max(F8 ? 3400 : 5400, 18 * cols + 1000) : blocks * (2200 + 17 * cols) + 300;
   }
 };
 
@@ -183,10 +195,10 @@ struct Ring {
 };
 
 template <bool F8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((kWarpConv + (F8 ? kConvWarps : 0)) * 32, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWarps<F8> * 32, 1)
 kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ CUtensorMap tm_ckv,
                    const __grid_constant__ CUtensorMap tm_kpe, const __grid_constant__ TcParams tp) {
-  constexpr int kThreads = (kWarpConv + (F8 ? kConvWarps : 0)) * 32;
+  constexpr int kThreads = kWarps<F8> * 32;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   Ctl& c = *reinterpret_cast<Ctl*>(sm + kRegion);
@@ -203,13 +215,12 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
     for (int i = 0; i < kMaxK; ++i) {
       mbar_init(&c.k_full[i], F8 ? 2 * (kConvWarps / kConvTeams) : 1);
       mbar_init(&c.k_empty[i], 1);
-      mbar_init(&c.conv_done[i], kConvWarps / kConvTeams);
     }
     for (int i = 0; i < kMaxQ; ++i) {
       mbar_init(&c.q_full[i], 1);
       mbar_init(&c.q_empty[i], 1);
     }
-    for (int i = 0; i < kRawSlots; ++i) {
+    for (int i = 0; i < kMaxRaw; ++i) {
       mbar_init(&c.raw_full[i], 1);
       mbar_init(&c.raw_empty[i], kConvWarps / kConvTeams);
     }
@@ -327,16 +338,15 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
     // -------------------------------------------------- key chunks (or codes) by TMA
     bool go = true;
     Ring ring;
-    if (F8) ring.restart(kRawSlots);
     const int oob = p.num_pages * kPage;  // past the pool: zeros
     for (; w.alive() && go; w.next()) {
-      if (!F8 && new_request(go)) ring.restart(w.sh.k_slots());
+      if (new_request(go)) ring.restart(F8 ? w.sh.raw_slots() : w.sh.k_slots());
       const int key = w.tile * kTileKeys + (int)rank * 128;
       int r0 = kw_pool_row(p, w.b, w.kv_len, key);
       int r1 = kw_pool_row(p, w.b, w.kv_len, key + kPage);
       r0 = r0 < 0 ? oob : r0;
       r1 = r1 < 0 ? oob : r1;
-      uint8_t* ring_at = F8 ? sm + kRegion - kRawSlots * kRawSlot : sm + w.sh.k_at();
+      uint8_t* ring_at = sm + (F8 ? w.sh.raw_at() : w.sh.k_at());
       for (int kc = 0; kc < kChunks && go; ++kc) {
         const int s = ring.slot;
         go = wait(F8 ? &c.raw_empty[s] : &c.k_empty[s], ring.phase() ^ 1);
@@ -362,9 +372,9 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
       }
     }
     // the last use of every slot must be over before the CTA may exit
-    for (int s = 0; s < (F8 ? kRawSlots : kMaxK) && go; ++s)
+    for (int s = 0; s < kMaxK && go; ++s)
       go = wait(F8 ? &c.raw_empty[s] : &c.k_empty[s], ((ring.used >> s) & 1u) ^ 1);
-    if (!F8 && go) wait(&c.seg_done, seg_parity);
+    if (go) wait(&c.seg_done, seg_parity);
     if (*abort) settle();
   } else if (warp == kWarpQ) {
     // ------------------------------------------------------------ query rows by TMA
@@ -484,34 +494,32 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
         final_wait(&c.drain, 0);
       }
     }
-  } else if (F8 && warp >= kWarpConv) {
+  } else if (F8 && warp >= kWarpConv<F8>) {
     // ------------------------------------------------------- FP8 codes to fp16 chunks
     // The teams work on different chunks at once, because a chunk's path (code wait,
     // loads, conversion, stores, proxy fence, arrival) takes over 1000 clocks.  Two
     // warps a team, 64 keys each: lane l has codes 16 (l & 3) .. of keys l / 4 + 8 i.
-    // A phase bit cannot tell a slot's last use from the one two before, and another
-    // team may still be at the last one: a team waits until that one is converted
-    // (conv_done) before it asks whether it is multiplied.  conv_done itself cannot be
-    // two behind: a chunk's codes arrive only when the chunks 5 and more before it
-    // have been read, so that their teams are done with the chunks 9 and more before,
-    // and two rounds of a ring are at least 10 chunks, or 8 of this team's own ring
-    // of 4; a new layout waits for all.
+    // A phase bit cannot tell a slot's last use from the one two before, so a team
+    // must not ask for a slot whose last use another team is still at: with 4 slots
+    // that was its own, and with 9 it is 9 chunks back, while codes arrive only when
+    // the chunks kRawBeside = 5 and more before them are converted.
     constexpr int kKeysPerWarp = 128 * kConvTeams / kConvWarps;
-    const int cw = warp - kWarpConv, team = cw % kConvTeams;
+    const int cw = warp - kWarpConv<F8>, team = cw % kConvTeams;
     const int m0 = cw / kConvTeams * kKeysPerWarp, sub = lane >> 2, u0 = lane & 3;
     const uint32_t full0 = map_to_rank(smem_u32(&c.k_full[0]), 0);
-    const uint8_t* codes = sm + kRegion - kRawSlots * kRawSlot + (m0 + sub) * 64 + u0 * 16;
     bool go = true;
     Ring raw, ring;
-    raw.restart(kRawSlots);
     int turn = 0;
     for (; w.alive() && go; w.next()) {
-      if (new_request(go)) ring.restart(w.sh.k_slots());
+      if (new_request(go)) {
+        ring.restart(w.sh.k_slots());
+        raw.restart(w.sh.raw_slots());
+      }
+      const uint8_t* codes = sm + w.sh.raw_at() + (m0 + sub) * 64 + u0 * 16;
       uint8_t* k_at = sm + w.sh.k_at() + (m0 + sub) * 128;
       for (int kc = 0; kc < kChunks && go; ++kc) {
         if (turn == team) {
           go = wait(&c.raw_full[raw.slot], raw.phase());
-          if (go) go = wait(&c.conv_done[ring.slot], ring.phase() ^ 1);
           if (go) go = wait(&c.k_empty[ring.slot], ring.phase() ^ 1);
           if (!go) break;
 #pragma unroll 2
@@ -535,7 +543,6 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
           __syncwarp();
           if (lane == 0) {
             arrive(&c.raw_empty[raw.slot]);
-            arrive(&c.conv_done[ring.slot]);
             arrive_cluster(full0 + ring.slot * 8);
           }
         }
@@ -546,17 +553,17 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
     }
     for (int s = 0; s < kMaxK && go; ++s) go = wait(&c.k_empty[s], ((ring.used >> s) & 1u) ^ 1);
     if (go) wait(&c.seg_done, seg_parity);
-  } else if (warp == kWarpInfo || warp == kWarpInfo + 1) {
+  } else if (warp >= kWarpInfo && warp < kWarpConv<F8>) {
     // ------------------------------------------------------- column data of each pass
-    // Ahead of the epilogue, so that their loads are off its path: one warp for each
-    // buffer, that is for every second pass.
+    // Ahead of the epilogue, so that their loads are off its path; two warps take
+    // turns.
     const int W = (p.T + 63) >> 6;
     uint32_t pass = 0;
     bool go = true;
     for (; w.alive() && go; w.next()) {
       for (int rb = 0; rb < w.sh.blocks && go; ++rb, ++pass) {
         const int buf = pass & 1;
-        if (buf != warp - kWarpInfo) continue;
+        if (kInfoWarps<F8> == 2 && buf != warp - kWarpInfo) continue;
         bool free = false;
 #pragma unroll 1
         for (int k0 = 0; k0 * 32 < w.sh.cols && go; k0 += 4) {
@@ -820,7 +827,7 @@ cudaError_t launch_kweights_tc(const va_key_weight_args& a, const KwParams& p, i
   auto* k = f8 ? kweights_tc_kernel<true> : kweights_tc_kernel<false>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
   if (e != cudaSuccess) return e;
-  const int threads = (kWarpConv + (f8 ? kConvWarps : 0)) * 32;
+  const int threads = (f8 ? kWarps<true> : kWarps<false>) * 32;
   k<<<2 * pairs, threads, kSmemBytes, st>>>(tq, tckv, tkpe, tp);
   return cudaGetLastError();
 }
