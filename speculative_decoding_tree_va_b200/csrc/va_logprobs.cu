@@ -5,18 +5,22 @@
 //   Z = sum 2^y_v     S = sum 2^y_v y_v
 //   lse = scale m + ln Z     lp_v = scale (x_v - m) - ln Z
 //   entropy = ln2 (log2 Z - S / Z)
-// x - m is taken before it is scaled: exact near the maximum, and a row whose
-// logits are all the type's lowest value still has differences of 0.  A
-// thread holds (m, Z, S) of what it has read and rescales them once per tile.
+// x - m is taken before it is scaled: exact near the maximum.  A thread holds
+// (m, Z, S) of what it has read and rescales them once per tile of its loads;
+// two elements go through each addition, product and multiply-add
+// (.f32x2).  Logits below -9.95e29 (masks) are read as that, so that no product
+// overflows; the rare row whose maximum is not within 9.95e29, or a scale over
+// 1e7, is summed again element by element without that.
 //
 // Top K: a candidate is a 64-bit key, the logit in order-preserving bits over
 // the complement of its index, so that equal logits order by lower index.
-// The K-th largest of the threads' maxima over the first tile is a lower
+// The K-th largest maximum of the half-warps over the first tile is a lower
 // bound of the row's K-th logit; a thread whose tile maximum reaches the bound
 // pushes the elements that do into a shared buffer, which is cut down to
 // its K largest (and the bound raised) when it holds more than kLimit.
 //
-// Bound by the one read of the logits from HBM.
+// Bound by the one read of the logits from HBM; the exponentials (16 a clock
+// and SM, 11.5 logits of bf16 arrive a clock) come next.
 #include <cfloat>
 
 #include "va_common.cuh"
@@ -27,9 +31,11 @@ namespace {
 constexpr int kNT = 256;     // threads per CTA
 constexpr int kU = 4;        // 16-byte vectors a thread holds per tile
 constexpr int kLimit = 256;  // candidates kept before they are cut down
+constexpr int kCap = 512;    // room for them
 constexpr int kMaxCluster = 8;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kFloor = -1.0e4f;  // 2^kFloor = 0; keeps 0 * y finite
+constexpr float kFar = 0x1.92p99f; // the fast sums' range of the maximum: 9.95e29, a bf16 value
 
 struct LpParams {
   const void* logits;
@@ -103,32 +109,83 @@ __device__ __forceinline__ uint4 load_stream(const uint4* p) {
   return v;
 }
 
+// Two fp32 values in one 64-bit register.
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
 template <typename T> struct Vec;  // a 16-byte vector of logits
 template <> struct Vec<float> {
   static constexpr int N = 4;
+  static constexpr uint32_t kNegInf = 0xff800000u;
   static __device__ __forceinline__ void unpack(const uint4& v, float (&x)[4]) {
     x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y);
     x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
   }
-  static __device__ __forceinline__ uint32_t bits(float x) { return __float_as_uint(x); }
-  static constexpr uint32_t kNegInf = 0xff800000u;
+  static __device__ __forceinline__ float largest(const uint4& v) {
+    float x[4];
+    unpack(v, x);
+    return max_nan(max_nan(x[0], x[1]), max_nan(x[2], x[3]));
+  }
+  // the same with nothing below -kFar
+  static __device__ __forceinline__ void unpack_near(const uint4& v, float (&x)[4]) {
+    unpack(v, x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = max_nan(x[i], -kFar);
+  }
 };
 template <> struct Vec<__nv_bfloat16> {
   static constexpr int N = 8;
-  static __device__ __forceinline__ void unpack(const uint4& v, float (&x)[8]) {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[2 * i] = __uint_as_float(w[i] << 16);
-      x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
   static constexpr uint32_t kNegInf = 0xff80ff80u;
+  static __device__ __forceinline__ void split(uint32_t w, float& a, float& b) {
+    a = __uint_as_float(w << 16);
+    b = __uint_as_float(w & 0xffff0000u);
+  }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  static __device__ __forceinline__ void unpack(const uint4& v, float (&x)[8]) {
+    split(v.x, x[0], x[1]);
+    split(v.y, x[2], x[3]);
+    split(v.z, x[4], x[5]);
+    split(v.w, x[6], x[7]);
+  }
+  static __device__ __forceinline__ float largest(const uint4& v) {
+    float a, b;
+    split(max2(max2(v.x, v.y), max2(v.z, v.w)), a, b);
+    return max_nan(a, b);
+  }
+  static __device__ __forceinline__ void unpack_near(const uint4& v, float (&x)[8]) {
+    constexpr uint32_t far = 0xf149f149u;  // -kFar
+    unpack(make_uint4(max2(v.x, far), max2(v.y, far), max2(v.z, far), max2(v.w, far)), x);
+  }
 };
 
 // Online sums of one thread: maximum, Z and S relative to it.
 struct Sums {
-  float m = -FLT_MAX, z = 0.f, s = 0.f;
+  float m = -kFar, z = 0.f, s = 0.f;
   __device__ __forceinline__ void raise(float to, float c) {  // to >= m, or NaN
     const float d = max_nan((m - to) * c, kFloor);
     const float f = ex2f(d);
@@ -191,14 +248,16 @@ __device__ void cut_down(uint64_t* cand, int n, int K, uint64_t* tmp) {
 // One row per cluster: CTA `rank` of C reads the rank-th part of the row's
 // vectors, rank 0 joins the parts over distributed shared memory.
 template <typename T>
-__global__ void __launch_bounds__(kNT) logprobs_kernel(const LpParams p, int C) {
+__global__ void __launch_bounds__(kNT, 4) logprobs_kernel(const LpParams p, int C) {
   using VT = Vec<T>;
   constexpr int N = VT::N;
-  extern __shared__ uint64_t cand[];  // kLimit + a tile's kNT * kU * N keys
+  constexpr int kHalves = kNT / 16;
+  __shared__ uint64_t cand[kCap];
   __shared__ uint64_t tmp[VA_MAX_TOPK];
   __shared__ float wm[kNT / 32], wz[kNT / 32], ws[kNT / 32];
-  __shared__ float part[3];           // this CTA's sums
-  __shared__ float tmax[kNT];
+  __shared__ float part[3], whole[3];  // this CTA's sums, the row's
+  __shared__ float hmax[kHalves];
+  __shared__ unsigned long long best;
   __shared__ int count;
   __shared__ float bound;
   __shared__ float fin[2];            // the row's maximum and ln Z
@@ -220,14 +279,11 @@ __global__ void __launch_bounds__(kNT) logprobs_kernel(const LpParams p, int C) 
   if (tid == 0) { count = 0; bound = -INFINITY; }
   __syncthreads();
 
-  Sums acc;
-  bool first = true;
-  for (int t0 = v0; t0 < v1; t0 += kNT * kU) {
-    uint4 raw[kU];
+  auto load = [&](int t0, uint4 (&raw)[kU]) {
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const int j = t0 + u * kNT + tid;
-      if (j < v1 && (j > 0 || off == 0) && (long long)(j + 1) * N - off <= V) {
+      if (j < v1 && (j > 0 || off == 0) && (j + 1) * N - off <= V) {
         raw[u] = load_stream(reinterpret_cast<const uint4*>(base) + j);
       } else {
         raw[u] = make_uint4(VT::kNegInf, VT::kNegInf, VT::kNegInf, VT::kNegInf);
@@ -236,64 +292,131 @@ __global__ void __launch_bounds__(kNT) logprobs_kernel(const LpParams p, int C) 
           *reinterpret_cast<uint4*>(e) = raw[u];
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            const long long v = (long long)j * N + i - off;
+            const int v = j * N + i - off;
             if (v >= 0 && v < V) e[i] = x0[v];
           }
           raw[u] = *reinterpret_cast<uint4*>(e);
         }
       }
     }
-    float mt = -INFINITY;
+  };
+  // calls f(x, index) for this thread's elements of a tile that are in the row
+  auto each = [&](int t0, const uint4 (&raw)[kU], auto f) {
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
+      const int j = t0 + u * kNT + tid;
+      if (j >= v1) continue;
       float x[N];
       VT::unpack(raw[u], x);
+      const int at = j * N - off;
 #pragma unroll
-      for (int i = 0; i < N; ++i) mt = max_nan(mt, x[i]);
+      for (int i = 0; i < N; ++i)
+        if (at + i >= 0 && at + i < V) f(x[i], at + i);
     }
-    if (!(mt <= acc.m)) acc.raise(mt, c);
-#pragma unroll
+  };
+
+  // the same from memory, element by element: for the rare paths, in little code
+  auto each_again = [&](int t0, auto f) {
+#pragma unroll 1
     for (int u = 0; u < kU; ++u) {
-      float x[N];
-      VT::unpack(raw[u], x);
+      const int j = t0 + u * kNT + tid;
+#pragma unroll 1
+      for (int i = 0; i < N; ++i) {
+        const int v = j * N + i - off;
+        if (j < v1 && v >= 0 && v < V) f(to_f32(x0[v]), v);
+      }
+    }
+  };
+
+  Sums acc;
+  const uint64_t c2 = pack2(c, c);
+  bool first = true;
+  for (int t0 = v0; t0 < v1; t0 += kNT * kU) {
+    uint4 raw[kU];
+    load(t0, raw);
+    float mt = VT::largest(raw[0]);
 #pragma unroll
-      for (int i = 0; i < N; ++i) acc.add(x[i], c);
+    for (int u = 1; u < kU; ++u) mt = max_nan(mt, VT::largest(raw[u]));
+    if (!(mt <= acc.m)) acc.raise(mt, c);
+    {
+      const uint64_t nm2 = pack2(-acc.m, -acc.m);
+      uint64_t z2 = pack2(acc.z, 0.f), s2 = pack2(acc.s, 0.f);
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        float x[N];
+        VT::unpack_near(raw[u], x);
+#pragma unroll
+        for (int i = 0; i < N; i += 2) {
+          const uint64_t y2 = mul2(add2(pack2(x[i], x[i + 1]), nm2), c2);
+          float ya, yb;
+          unpack2(y2, ya, yb);
+          const uint64_t e2 = pack2(ex2f(ya), ex2f(yb));
+          z2 = add2(z2, e2);
+          s2 = fma2(e2, y2, s2);
+        }
+      }
+      float za, zb, sa, sb;
+      unpack2(z2, za, zb);
+      unpack2(s2, sa, sb);
+      acc.z = za + zb;
+      acc.s = sa + sb;
     }
     if (K > 0) {
       if (first) {
-        // the K-th largest thread maximum (ties by thread) bounds the K-th logit
-        tmax[tid] = mt;
+        // the K-th largest half-warp maximum (ties by half-warp) bounds the K-th logit
+        float hm = mt == mt ? mt : -INFINITY;
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) hm = fmaxf(hm, __shfl_xor_sync(kFull, hm, d));
+        if ((lane & 15) == 0) hmax[tid >> 4] = hm;
         __syncthreads();
-        const uint32_t mine = order_bits(mt);
-        int r = 0;
-        for (int i = 0; i < kNT; ++i) {
-          const uint32_t o = order_bits(tmax[i]);
-          r += o > mine || (o == mine && i < tid);
+        if (tid < kHalves) {
+          const float mine = hmax[tid];
+          int r = 0;
+          for (int i = 0; i < kHalves; ++i) r += hmax[i] > mine || (hmax[i] == mine && i < tid);
+          if (r == K - 1) bound = mine;
         }
-        if (r == K - 1 && mt > -INFINITY) bound = mt;
         __syncthreads();
         first = false;
       }
       bool full = false;
       const float b = bound;
-      if (mt >= b) {
-#pragma unroll
-        for (int u = 0; u < kU; ++u) {
-          float x[N];
-          VT::unpack(raw[u], x);
-          const long long at = (long long)(t0 + u * kNT + tid) * N - off;
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            if (x[i] >= b && t0 + u * kNT + tid < v1 && at + i >= 0 && at + i < V) {
-              const int n = atomicAdd(&count, 1);
-              cand[n] = make_key(x[i], (int)(at + i));
-              full |= n >= kLimit;
-            }
+      if (mt >= b)
+        each(t0, raw, [&](float x, int v) {
+          if (x >= b) {
+            const int n = atomicAdd(&count, 1);
+            if (n < kCap) cand[n] = make_key(x, v);
+            full |= n >= kLimit;
           }
-        }
-      }
+        });
       if (__syncthreads_or(full)) {
-        cut_down(cand, count, K, tmp);
+        if (count <= kCap) {
+          cut_down(cand, count, K, tmp);
+        } else {
+          // More than fit (equal logits, or rows that rise): K rounds of the largest
+          // key below the last one, of the buffer's and of the tile's, which may
+          // hold the same key twice.
+          uint64_t below = ~0ull;
+          for (int r = 0; r < K; ++r) {
+            if (tid == 0) best = 0;
+            __syncthreads();
+            uint64_t mine = 0;
+            for (int i = tid; i < kCap; i += kNT)
+              if (cand[i] < below && cand[i] > mine) mine = cand[i];
+            each_again(t0, [&](float x, int v) {
+              if (x >= b) {
+                const uint64_t k = make_key(x, v);
+                if (k < below && k > mine) mine = k;
+              }
+            });
+            if (mine) atomicMax(&best, (unsigned long long)mine);
+            __syncthreads();
+            below = best;
+            if (tid == 0) tmp[r] = below;
+            __syncthreads();
+          }
+          if (tid < K) cand[tid] = tmp[tid];
+          __syncthreads();
+        }
         if (tid == 0) {
           count = K;
           bound = order_value((uint32_t)(cand[K - 1] >> 32));
@@ -304,56 +427,80 @@ __global__ void __launch_bounds__(kNT) logprobs_kernel(const LpParams p, int C) 
   }
   if (K > 0) cut_down(cand, count, K, tmp);
 
-  // join the threads' sums: lanes, then warps
+  // join the threads' sums in part[]: lanes, then warps
+  auto join_cta = [&]() {
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) {
-    Sums o;
-    o.m = __shfl_xor_sync(kFull, acc.m, d);
-    o.z = __shfl_xor_sync(kFull, acc.z, d);
-    o.s = __shfl_xor_sync(kFull, acc.s, d);
-    acc.join(o, c);
-  }
-  if (lane == 0) { wm[warp] = acc.m; wz[warp] = acc.z; ws[warp] = acc.s; }
-  __syncthreads();
-  if (tid == 0) {
-    Sums a;
-    for (int w = 0; w < kNT / 32; ++w) {
+    for (int d = 16; d > 0; d >>= 1) {
       Sums o;
-      o.m = wm[w]; o.z = wz[w]; o.s = ws[w];
-      a.join(o, c);
+      o.m = __shfl_xor_sync(kFull, acc.m, d);
+      o.z = __shfl_xor_sync(kFull, acc.z, d);
+      o.s = __shfl_xor_sync(kFull, acc.s, d);
+      acc.join(o, c);
     }
-    part[0] = a.m; part[1] = a.z; part[2] = a.s;
+    if (lane == 0) { wm[warp] = acc.m; wz[warp] = acc.z; ws[warp] = acc.s; }
+    __syncthreads();
+    if (tid == 0) {
+      Sums a;
+      a.m = wm[0]; a.z = wz[0]; a.s = ws[0];
+      for (int w = 1; w < kNT / 32; ++w) {
+        Sums o;
+        o.m = wm[w]; o.z = wz[w]; o.s = ws[w];
+        a.join(o, c);
+      }
+      part[0] = a.m; part[1] = a.z; part[2] = a.s;
+    }
+    if (C > 1) cluster_sync_all();  // part[] (and cand[0, K)) of every CTA are in place
+    else __syncthreads();
+  };
+  join_cta();
+  float row_max = part[0];
+  if (C > 1)
+    for (int r = 0; r < C; ++r) row_max = max_nan(row_max, remote_f32(&part[0], r));
+  const bool far = row_max <= -kFar || (row_max > kFar && row_max < INFINITY) || p.scale > 1e7f;
+  if (far) {  // the same for all CTAs of the row: sum again, element by element
+    acc.m = -FLT_MAX;
+    acc.z = acc.s = 0.f;
+    for (int t0 = v0; t0 < v1; t0 += kNT * kU)
+      each_again(t0, [&](float x, int) {
+        if (x > acc.m) acc.raise(x, c);
+        acc.add(x, c);
+      });
+    if (C > 1) cluster_sync_all();  // the first sums have been read everywhere
+    else __syncthreads();
+    join_cta();
   }
   if (C > 1) {
-    cluster_sync_all();  // every CTA's part[] and cand[0, K) are in place
     if (rank == 0) {
       if (tid == 0) {
         Sums a;
-        for (int r = 0; r < C; ++r) {
+        a.m = part[0]; a.z = part[1]; a.s = part[2];
+        for (int r = 1; r < C; ++r) {
           Sums o;
           o.m = remote_f32(&part[0], r);
           o.z = remote_f32(&part[1], r);
           o.s = remote_f32(&part[2], r);
           a.join(o, c);
         }
-        part[0] = a.m; part[1] = a.z; part[2] = a.s;
+        whole[0] = a.m; whole[1] = a.z; whole[2] = a.s;
       }
       if (tid >= K && tid < C * K) cand[tid] = remote_u64(&cand[tid % K], tid / K);
     }
     cluster_sync_all();  // remote reads are done: the other CTAs may exit
     if (rank != 0) return;
     if (K > 0) cut_down(cand, C * K, K, tmp);
+  } else if (tid == 0) {
+    whole[0] = part[0]; whole[1] = part[1]; whole[2] = part[2];
   }
   __syncthreads();
   if (tid == 0) {
-    const float m = part[0], z = part[1];
-    const bool bad = !(z == z) || m == INFINITY;
+    const float m = whole[0], z = whole[1];
+    const bool bad = !(z == z) || !(m == m) || m == INFINITY;
     const float lnz = logf(z);  // z = 0 (no finite logit): -inf
     fin[0] = m;
     fin[1] = bad ? NAN : lnz;
     if (p.lse) p.lse[row] = bad ? NAN : (z > 0.f ? fmaf(m, p.scale, lnz) : -INFINITY);
     if (p.entropy)
-      p.entropy[row] = bad ? NAN : (z > 0.f ? fmaxf(lnz - kLn2 * (part[2] / z), 0.f) : 0.f);
+      p.entropy[row] = bad ? NAN : (z > 0.f ? fmaxf(lnz - kLn2 * (whole[2] / z), 0.f) : 0.f);
     if (bad && p.row_status) p.row_status[row] = VA_ERR_INVALID_ARG;
   }
   __syncthreads();
@@ -384,13 +531,6 @@ __global__ void __launch_bounds__(kNT) logprobs_kernel(const LpParams p, int C) 
 
 template <typename T>
 cudaError_t launch(const LpParams& p, int R, int C, cudaStream_t st) {
-  constexpr int kCandBytes = (kLimit + kNT * kU * Vec<T>::N) * (int)sizeof(uint64_t);
-  const size_t smem = p.K > 0 ? kCandBytes : 0;
-  if (smem > 40 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(logprobs_kernel<T>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, kCandBytes);
-    if (e != cudaSuccess) return e;
-  }
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = C;
@@ -399,7 +539,6 @@ cudaError_t launch(const LpParams& p, int R, int C, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((long long)R * C));
   cfg.blockDim = dim3(kNT);
-  cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = C > 1 ? 1 : 0;
@@ -425,10 +564,10 @@ cudaError_t launch_logprobs(const va_logprob_args& a, int sms, cudaStream_t st) 
   p.top_lp64 = a.top_lp64;
   p.row_status = a.row_status;
   // Few rows: a row is cut over a cluster while its CTAs keep more than one
-  // tile each and the SMs are not yet covered.
+  // tile each and the SMs do not yet hold two CTAs each.
   const long long tile = (long long)kNT * kU * (a.dtype == VA_F32 ? 4 : 8);
   int C = 1;
-  while (C < kMaxCluster && (long long)a.R * C < sms && (long long)a.V > tile * C) C *= 2;
+  while (C < kMaxCluster && (long long)a.R * C < 2 * sms && (long long)a.V > tile * C) C *= 2;
   return a.dtype == VA_F32 ? launch<float>(p, a.R, C, st) : launch<__nv_bfloat16>(p, a.R, C, st);
 }
 
