@@ -14,10 +14,12 @@
 //
 // Top K: a candidate is a 64-bit key, the logit in order-preserving bits over
 // the complement of its index, so that equal logits order by lower index.
-// The K-th largest maximum of the half-warps over the first tile is a lower
-// bound of the row's K-th logit; a thread whose tile maximum reaches the bound
-// pushes the elements that do into a shared buffer, which is cut down to
-// its K largest (and the bound raised) when it holds more than kLimit.
+// Each warp keeps a list in shared memory.  The K-th largest of its lanes'
+// maxima over its first tile is a lower bound of the row's K-th logit, so a
+// lane pushes only the elements of a later tile that reach the largest bound
+// any warp has found; a list that grows past kCut is cut down to its K largest,
+// which raises the bound.  Warps wait for each other only at the row's end,
+// and a warp's next tile is on its way while one is worked on.
 //
 // Bound by the one read of the logits from HBM; the exponentials (16 a clock
 // and SM, 11.5 logits of bf16 arrive a clock) come next.
@@ -29,10 +31,12 @@ namespace va {
 namespace {
 
 constexpr int kNT = 256;     // threads per CTA
-constexpr int kU = 4;        // 16-byte vectors a thread holds per tile
-constexpr int kLimit = 256;  // candidates kept before they are cut down
-constexpr int kCap = 512;    // room for them
+constexpr int kWarps = kNT / 32;
+constexpr int kU = 4;        // 16-byte vectors a lane holds per tile
+constexpr int kCut = 64;     // candidates of a warp before they are cut down
+constexpr int kCap = 128;    // room for them
 constexpr int kMaxCluster = 8;
+static_assert(kMaxCluster * VA_MAX_TOPK <= kNT && kWarps * VA_MAX_TOPK <= kNT, "cut_down");
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kFloor = -1.0e4f;  // 2^kFloor = 0; keeps 0 * y finite
 constexpr float kFar = 0x1.92p99f; // the fast sums' range of the maximum: 9.95e29, a bf16 value
@@ -210,57 +214,62 @@ struct Sums {
   }
 };
 
-// Cuts cand[0, n) to its K largest keys, descending, in cand[0, K) (0 where
-// there are fewer).  Called by the whole CTA; all keys are distinct.
-__device__ void cut_down(uint64_t* cand, int n, int K, uint64_t* tmp) {
+// Cuts cand[0, n), n <= kNT, to its K largest keys, descending, in cand[0, K)
+// (0 where there are fewer).  Called by the whole CTA; the keys other than 0
+// are distinct.
+__device__ void cut_down(uint64_t* cand, int n, int K) {
   const int tid = threadIdx.x;
-  if (tid < VA_MAX_TOPK) tmp[tid] = 0;
+  const uint64_t k = tid < n ? cand[tid] : 0;
+  int r = 0;
+  if (k)
+    for (int i = 0; i < n; ++i) r += cand[i] > k;
   __syncthreads();
-  if (n <= kNT) {  // rank of each key among all
-    if (tid < n) {
-      const uint64_t k = cand[tid];
-      int r = 0;
-      for (int i = 0; i < n; ++i) r += cand[i] > k;
-      if (r < K) tmp[r] = k;
-    }
-  } else {  // crowded (many equal logits): K rounds of the largest key below the last
-    __shared__ unsigned long long best;
-    uint64_t below = ~0ull;
-    for (int r = 0; r < K; ++r) {
-      if (tid == 0) best = 0;
-      __syncthreads();
-      unsigned long long mine = 0;
-      for (int i = tid; i < n; i += kNT)
-        if (cand[i] < below && cand[i] > mine) mine = cand[i];
-      if (mine) atomicMax(&best, mine);
-      __syncthreads();
-      below = best;
-      if (tid == 0) tmp[r] = below;
-      __syncthreads();
-      if (below == 0) break;
-    }
+  if (tid < K) cand[tid] = 0;
+  __syncthreads();
+  if (k && r < K) cand[r] = k;
+  __syncthreads();
+}
+
+// The same by one warp, n <= kCap.
+__device__ void warp_cut(uint64_t* cand, int n, int K) {
+  constexpr int kPer = kCap / 32;
+  const int lane = threadIdx.x & 31;
+  uint64_t k[kPer];
+  int r[kPer];
+#pragma unroll
+  for (int q = 0; q < kPer; ++q) {
+    k[q] = lane + 32 * q < n ? cand[lane + 32 * q] : 0;
+    r[q] = 0;
   }
-  __syncthreads();
-  if (tid < K) cand[tid] = tmp[tid];
-  __syncthreads();
+  for (int i = 0; i < n; ++i) {
+    const uint64_t o = cand[i];
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) r[q] += o > k[q];
+  }
+  __syncwarp();
+  if (lane < K) cand[lane] = 0;
+  __syncwarp();
+#pragma unroll
+  for (int q = 0; q < kPer; ++q)
+    if (k[q] && r[q] < K) cand[r[q]] = k[q];
+  __syncwarp();
 }
 
 // One row per cluster: CTA `rank` of C reads the rank-th part of the row's
 // vectors, rank 0 joins the parts over distributed shared memory.
 template <typename T>
-__global__ void __launch_bounds__(kNT, 4) logprobs_kernel(const LpParams p, int C) {
+__global__ void __launch_bounds__(kNT, 3) logprobs_kernel(const LpParams p, int C) {
   using VT = Vec<T>;
   constexpr int N = VT::N;
-  constexpr int kHalves = kNT / 16;
-  __shared__ uint64_t cand[kCap];
-  __shared__ uint64_t tmp[VA_MAX_TOPK];
-  __shared__ float wm[kNT / 32], wz[kNT / 32], ws[kNT / 32];
-  __shared__ float part[3], whole[3];  // this CTA's sums, the row's
-  __shared__ float hmax[kHalves];
-  __shared__ unsigned long long best;
-  __shared__ int count;
-  __shared__ float bound;
-  __shared__ float fin[2];            // the row's maximum and ln Z
+  constexpr int kStep = kWarps * kU * 32;  // vectors of the CTA's tiles side by side
+  __shared__ uint64_t lists[kWarps][kCap];
+  __shared__ uint64_t kth[kWarps];         // a warp's K-th key so far
+  __shared__ uint64_t cand[kNT];
+  __shared__ int counts[kWarps];
+  __shared__ uint32_t bound;               // order_bits of the largest bound
+  __shared__ float wm[kWarps], wz[kWarps], ws[kWarps];
+  __shared__ float part[3], whole[3];      // this CTA's sums, the row's
+  __shared__ float fin[2];                 // the row's maximum and ln Z
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t rank = C > 1 ? cluster_rank() : 0;
   const long long row = blockIdx.x / C;
@@ -274,15 +283,17 @@ __global__ void __launch_bounds__(kNT, 4) logprobs_kernel(const LpParams p, int 
   const int nv = (int)(((long long)V + off + N - 1) / N);
   const int per = (nv + C - 1) / C;
   const int v0 = min(nv, (int)rank * per), v1 = min(nv, v0 + per);
+  const int w0 = v0 + warp * kU * 32;      // this warp's first tile
   const float c = p.scale * kLog2e;
 
-  if (tid == 0) { count = 0; bound = -INFINITY; }
+  if (tid == 0) bound = order_bits(-INFINITY);
+  if (lane == 0) { counts[warp] = 0; kth[warp] = 0; }
   __syncthreads();
 
   auto load = [&](int t0, uint4 (&raw)[kU]) {
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      const int j = t0 + u * kNT + tid;
+      const int j = t0 + u * 32 + lane;
       if (j < v1 && (j > 0 || off == 0) && (j + 1) * N - off <= V) {
         raw[u] = load_stream(reinterpret_cast<const uint4*>(base) + j);
       } else {
@@ -300,26 +311,12 @@ __global__ void __launch_bounds__(kNT, 4) logprobs_kernel(const LpParams p, int 
       }
     }
   };
-  // calls f(x, index) for this thread's elements of a tile that are in the row
-  auto each = [&](int t0, const uint4 (&raw)[kU], auto f) {
-#pragma unroll
-    for (int u = 0; u < kU; ++u) {
-      const int j = t0 + u * kNT + tid;
-      if (j >= v1) continue;
-      float x[N];
-      VT::unpack(raw[u], x);
-      const int at = j * N - off;
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (at + i >= 0 && at + i < V) f(x[i], at + i);
-    }
-  };
-
-  // the same from memory, element by element: for the rare paths, in little code
+  // calls f(x, index) for this lane's elements of a tile that are in the row; read
+  // again from memory, element by element: for the rare paths, in little code
   auto each_again = [&](int t0, auto f) {
 #pragma unroll 1
     for (int u = 0; u < kU; ++u) {
-      const int j = t0 + u * kNT + tid;
+      const int j = t0 + u * 32 + lane;
 #pragma unroll 1
       for (int i = 0; i < N; ++i) {
         const int v = j * N + i - off;
@@ -330,10 +327,10 @@ __global__ void __launch_bounds__(kNT, 4) logprobs_kernel(const LpParams p, int 
 
   Sums acc;
   const uint64_t c2 = pack2(c, c);
-  bool first = true;
-  for (int t0 = v0; t0 < v1; t0 += kNT * kU) {
-    uint4 raw[kU];
-    load(t0, raw);
+  uint4 raw[kU], next[kU];
+  if (w0 < v1) load(w0, raw);
+  for (int t0 = w0; t0 < v1; t0 += kStep) {
+    if (t0 + kStep < v1) load(t0 + kStep, next);
     float mt = VT::largest(raw[0]);
 #pragma unroll
     for (int u = 1; u < kU; ++u) mt = max_nan(mt, VT::largest(raw[u]));
@@ -362,70 +359,88 @@ __global__ void __launch_bounds__(kNT, 4) logprobs_kernel(const LpParams p, int 
       acc.s = sa + sb;
     }
     if (K > 0) {
-      if (first) {
-        // the K-th largest half-warp maximum (ties by half-warp) bounds the K-th logit
-        float hm = mt == mt ? mt : -INFINITY;
+      const float top = mt == mt ? mt : -INFINITY;
+      if (t0 == w0) {  // the K-th largest lane maximum (ties by lane)
+        int r = 0;
 #pragma unroll
-        for (int d = 8; d > 0; d >>= 1) hm = fmaxf(hm, __shfl_xor_sync(kFull, hm, d));
-        if ((lane & 15) == 0) hmax[tid >> 4] = hm;
-        __syncthreads();
-        if (tid < kHalves) {
-          const float mine = hmax[tid];
-          int r = 0;
-          for (int i = 0; i < kHalves; ++i) r += hmax[i] > mine || (hmax[i] == mine && i < tid);
-          if (r == K - 1) bound = mine;
+        for (int i = 0; i < 32; ++i) {
+          const float o = __shfl_sync(kFull, top, i);
+          r += o > top || (o == top && i < lane);
         }
-        __syncthreads();
-        first = false;
+        if (r == K - 1) atomicMax(&bound, order_bits(top));
+        __syncwarp();
       }
-      bool full = false;
-      const float b = bound;
-      if (mt >= b)
-        each(t0, raw, [&](float x, int v) {
-          if (x >= b) {
-            const int n = atomicAdd(&count, 1);
-            if (n < kCap) cand[n] = make_key(x, v);
-            full |= n >= kLimit;
-          }
-        });
-      if (__syncthreads_or(full)) {
-        if (count <= kCap) {
-          cut_down(cand, count, K, tmp);
-        } else {
-          // More than fit (equal logits, or rows that rise): K rounds of the largest
-          // key below the last one, of the buffer's and of the tile's, which may
-          // hold the same key twice.
-          uint64_t below = ~0ull;
-          for (int r = 0; r < K; ++r) {
-            if (tid == 0) best = 0;
-            __syncthreads();
-            uint64_t mine = 0;
-            for (int i = tid; i < kCap; i += kNT)
-              if (cand[i] < below && cand[i] > mine) mine = cand[i];
-            each_again(t0, [&](float x, int v) {
-              if (x >= b) {
-                const uint64_t k = make_key(x, v);
-                if (k < below && k > mine) mine = k;
+      const float b = order_value(*(volatile uint32_t*)&bound);
+      if (__any_sync(kFull, top >= b)) {
+        const uint64_t floor = kth[warp];
+        if (top >= b) {
+#pragma unroll
+          for (int u = 0; u < kU; ++u) {
+            const int j = t0 + u * 32 + lane;
+            const int at = j * N - off;
+            float x[N];
+            VT::unpack(raw[u], x);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+              if (x[i] >= b && j < v1 && at + i >= 0 && at + i < V) {
+                const uint64_t k = make_key(x[i], at + i);
+                if (k > floor) {
+                  const int n = atomicAdd(&counts[warp], 1);
+                  if (n < kCap) lists[warp][n] = k;
+                }
               }
-            });
-            if (mine) atomicMax(&best, (unsigned long long)mine);
-            __syncthreads();
-            below = best;
-            if (tid == 0) tmp[r] = below;
-            __syncthreads();
+            }
           }
-          if (tid < K) cand[tid] = tmp[tid];
-          __syncthreads();
         }
-        if (tid == 0) {
-          count = K;
-          bound = order_value((uint32_t)(cand[K - 1] >> 32));
+        __syncwarp();
+        const int n = *(volatile int*)&counts[warp];
+        if (n > kCut) {
+          if (n <= kCap) {
+            warp_cut(lists[warp], n, K);
+          } else {
+            // More than fit (equal logits, or rows that rise): K rounds of the
+            // largest key below the last one, of the list's and of the tile's,
+            // which may hold the same key twice.
+            uint64_t below = ~0ull, mine_at = 0;
+            for (int r = 0; r < K; ++r) {
+              uint64_t mine = 0;
+              for (int i = lane; i < kCap; i += 32)
+                if (lists[warp][i] < below && lists[warp][i] > mine) mine = lists[warp][i];
+              each_again(t0, [&](float x, int v) {
+                if (x >= b) {
+                  const uint64_t k = make_key(x, v);
+                  if (k < below && k > mine) mine = k;
+                }
+              });
+              const uint32_t hi = __reduce_max_sync(kFull, (uint32_t)(mine >> 32));
+              const uint32_t lo = __reduce_max_sync(
+                  kFull, (uint32_t)(mine >> 32) == hi ? (uint32_t)mine : 0u);
+              below = (uint64_t)hi << 32 | lo;
+              if (lane == r) mine_at = below;
+            }
+            __syncwarp();
+            if (lane < K) lists[warp][lane] = mine_at;
+            __syncwarp();
+          }
+          if (lane == 0) {
+            const uint64_t k = lists[warp][K - 1];
+            counts[warp] = K;
+            kth[warp] = k;
+            atomicMax(&bound, (uint32_t)(k >> 32));
+          }
+          __syncwarp();
         }
-        __syncthreads();
       }
     }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) raw[u] = next[u];
   }
-  if (K > 0) cut_down(cand, count, K, tmp);
+  if (K > 0) {
+    warp_cut(lists[warp], counts[warp], K);
+    if (lane < K) cand[warp * K + lane] = lists[warp][lane];
+    __syncthreads();
+    cut_down(cand, kWarps * K, K);
+  }
 
   // join the threads' sums in part[]: lanes, then warps
   auto join_cta = [&]() {
@@ -442,7 +457,7 @@ __global__ void __launch_bounds__(kNT, 4) logprobs_kernel(const LpParams p, int 
     if (tid == 0) {
       Sums a;
       a.m = wm[0]; a.z = wz[0]; a.s = ws[0];
-      for (int w = 1; w < kNT / 32; ++w) {
+      for (int w = 1; w < kWarps; ++w) {
         Sums o;
         o.m = wm[w]; o.z = wz[w]; o.s = ws[w];
         a.join(o, c);
@@ -460,7 +475,7 @@ __global__ void __launch_bounds__(kNT, 4) logprobs_kernel(const LpParams p, int 
   if (far) {  // the same for all CTAs of the row: sum again, element by element
     acc.m = -FLT_MAX;
     acc.z = acc.s = 0.f;
-    for (int t0 = v0; t0 < v1; t0 += kNT * kU)
+    for (int t0 = w0; t0 < v1; t0 += kStep)
       each_again(t0, [&](float x, int) {
         if (x > acc.m) acc.raise(x, c);
         acc.add(x, c);
@@ -487,7 +502,7 @@ __global__ void __launch_bounds__(kNT, 4) logprobs_kernel(const LpParams p, int 
     }
     cluster_sync_all();  // remote reads are done: the other CTAs may exit
     if (rank != 0) return;
-    if (K > 0) cut_down(cand, C * K, K, tmp);
+    if (K > 0) cut_down(cand, C * K, K);
   } else if (tid == 0) {
     whole[0] = part[0]; whole[1] = part[1]; whole[2] = part[2];
   }
