@@ -1,16 +1,17 @@
 // Log probabilities of given tokens, entropy and top alternatives of rows of
 // logits: the drafter's per-depth top-k and the target's greedy tokens.
 //
-// With m the row's maximum, c = scale log2(e) and y_v = c (x_v - m) <= 0:
-//   Z = sum 2^y_v     S = sum 2^y_v y_v
-//   lse = scale m + ln Z     lp_v = scale (x_v - m) - ln Z
+// With m the row's maximum, c = scale log2(e) and y_v = c x_v - r, where r is
+// c m rounded to fp32 and eps = c m - r (exact, a multiply-add away):
+//   Z = sum 2^y_v     S = sum 2^y_v y_v     ln Z' = ln Z - eps ln2
+//   lse = scale m + ln Z'     lp_v = scale (x_v - m) - ln Z'
 //   entropy = ln2 (log2 Z - S / Z)
-// x - m is taken before it is scaled: exact near the maximum.  A thread holds
-// (m, Z, S) of what it has read and rescales them once per tile of its loads;
-// two elements go through each addition, product and multiply-add
-// (.f32x2).  Logits below -9.95e29 (masks) are read as that, so that no product
-// overflows; the rare row whose maximum is not within 9.95e29, or a scale over
-// 1e7, is summed again element by element without that.
+// y_v is one rounding of its value, so a common r costs no accuracy.  A thread
+// holds (m, Z, S) of what it has read and rescales them once per tile of its
+// loads; two elements go through each addition and multiply-add (.f32x2).
+// Logits below -9.95e29 (masks) are read as that, so that no product overflows;
+// the rare row whose maximum is not within 9.95e29, or a scale over 1e7, is
+// summed again element by element with y_v = c (x_v - m) and eps = 0.
 //
 // Top K: a candidate is a 64-bit key, the logit in order-preserving bits over
 // the complement of its index, so that equal logits order by lower index.
@@ -18,12 +19,14 @@
 // maxima over its first tile is a lower bound of the row's K-th logit, so a
 // lane pushes only the elements of a later tile that reach the largest bound
 // any warp has found; a list that grows past kCut is cut down to its K largest,
-// which raises the bound.  Warps wait for each other only at the row's end,
-// and a warp's next tile is on its way while one is worked on.
+// which raises the bound.  Warps wait for each other only at the row's end.
+// (Loading a tile ahead costs registers and with them a CTA per SM: 124 us
+// against 126 for 2112 rows of 131072, but 16.5 against 14.4 for 960 of 4096.)
 //
 // Bound by the one read of the logits from HBM; the exponentials (16 a clock
 // and SM, 11.5 logits of bf16 arrive a clock) come next.
 #include <cfloat>
+#include <type_traits>
 
 #include "va_common.cuh"
 
@@ -127,11 +130,6 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
@@ -146,10 +144,15 @@ template <> struct Vec<float> {
     x[0] = __uint_as_float(v.x); x[1] = __uint_as_float(v.y);
     x[2] = __uint_as_float(v.z); x[3] = __uint_as_float(v.w);
   }
-  static __device__ __forceinline__ float largest(const uint4& v) {
-    float x[4];
-    unpack(v, x);
-    return max_nan(max_nan(x[0], x[1]), max_nan(x[2], x[3]));
+  template <int U> static __device__ __forceinline__ float largest(const uint4 (&v)[U]) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      float x[4];
+      unpack(v[u], x);
+      m = max_nan(m, max_nan(max_nan(x[0], x[1]), max_nan(x[2], x[3])));
+    }
+    return m;
   }
   // the same with nothing below -kFar
   static __device__ __forceinline__ void unpack_near(const uint4& v, float (&x)[4]) {
@@ -176,9 +179,12 @@ template <> struct Vec<__nv_bfloat16> {
     split(v.z, x[4], x[5]);
     split(v.w, x[6], x[7]);
   }
-  static __device__ __forceinline__ float largest(const uint4& v) {
+  template <int U> static __device__ __forceinline__ float largest(const uint4 (&v)[U]) {
+    uint32_t m = kNegInf;
+#pragma unroll
+    for (int u = 0; u < U; ++u) m = max2(m, max2(max2(v[u].x, v[u].y), max2(v[u].z, v[u].w)));
     float a, b;
-    split(max2(max2(v.x, v.y), max2(v.z, v.w)), a, b);
+    split(m, a, b);
     return max_nan(a, b);
   }
   static __device__ __forceinline__ void unpack_near(const uint4& v, float (&x)[8]) {
@@ -187,30 +193,27 @@ template <> struct Vec<__nv_bfloat16> {
   }
 };
 
-// Online sums of one thread: maximum, Z and S relative to it.
+// Online sums of one thread: maximum, Z and S relative to it (`Far`: of the
+// second way above).
 struct Sums {
   float m = -kFar, z = 0.f, s = 0.f;
+  template <bool Far>
   __device__ __forceinline__ void raise(float to, float c) {  // to >= m, or NaN
-    const float d = max_nan((m - to) * c, kFloor);
+    const float way = Far ? (m - to) * c : __fmul_rn(m, c) - __fmul_rn(to, c);
+    const float d = max_nan(way, kFloor);
     const float f = ex2f(d);
     s = f * fmaf(z, d, s);
     z *= f;
     m = to;
   }
-  __device__ __forceinline__ void add(float x, float c) {
-    const float y = max_nan((x - m) * c, kFloor);
-    const float e = ex2f(y);
-    z += e;
-    s = fmaf(e, y, s);
-  }
+  template <bool Far>
   __device__ __forceinline__ void join(const Sums& o, float c) {
-    Sums a = *this, b = o;
-    const float to = max_nan(a.m, b.m);
-    a.raise(to, c);
-    b.raise(to, c);
-    m = to;
-    z = a.z + b.z;
-    s = a.s + b.s;
+    Sums b = o;
+    const float to = max_nan(m, b.m);
+    raise<Far>(to, c);
+    b.raise<Far>(to, c);
+    z += b.z;
+    s += b.s;
   }
 };
 
@@ -258,14 +261,14 @@ __device__ void warp_cut(uint64_t* cand, int n, int K) {
 // One row per cluster: CTA `rank` of C reads the rank-th part of the row's
 // vectors, rank 0 joins the parts over distributed shared memory.
 template <typename T>
-__global__ void __launch_bounds__(kNT, 3) logprobs_kernel(const LpParams p, int C) {
+__global__ void __launch_bounds__(kNT, 4) logprobs_kernel(const LpParams p, int C) {
   using VT = Vec<T>;
   constexpr int N = VT::N;
   constexpr int kStep = kWarps * kU * 32;  // vectors of the CTA's tiles side by side
   __shared__ uint64_t lists[kWarps][kCap];
   __shared__ uint64_t kth[kWarps];         // a warp's K-th key so far
   __shared__ uint64_t cand[kNT];
-  __shared__ int counts[kWarps];
+  __shared__ int counts[kWarps], total;
   __shared__ uint32_t bound;               // order_bits of the largest bound
   __shared__ float wm[kWarps], wz[kWarps], ws[kWarps];
   __shared__ float part[3], whole[3];      // this CTA's sums, the row's
@@ -286,11 +289,18 @@ __global__ void __launch_bounds__(kNT, 3) logprobs_kernel(const LpParams p, int 
   const int w0 = v0 + warp * kU * 32;      // this warp's first tile
   const float c = p.scale * kLog2e;
 
-  if (tid == 0) bound = order_bits(-INFINITY);
+  if (tid == 0) { bound = order_bits(-INFINITY); total = 0; }
   if (lane == 0) { counts[warp] = 0; kth[warp] = 0; }
   __syncthreads();
 
+  const int whole_to = min(v1, (V + off) / N);  // vectors [off > 0, whole_to) lie in the row
   auto load = [&](int t0, uint4 (&raw)[kU]) {
+    if (t0 >= (off > 0) && t0 + kU * 32 <= whole_to) {
+      const uint4* at = reinterpret_cast<const uint4*>(base) + t0 + lane;
+#pragma unroll
+      for (int u = 0; u < kU; ++u) raw[u] = load_stream(at + u * 32);
+      return;
+    }
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       const int j = t0 + u * 32 + lane;
@@ -327,16 +337,14 @@ __global__ void __launch_bounds__(kNT, 3) logprobs_kernel(const LpParams p, int 
 
   Sums acc;
   const uint64_t c2 = pack2(c, c);
-  uint4 raw[kU], next[kU];
-  if (w0 < v1) load(w0, raw);
   for (int t0 = w0; t0 < v1; t0 += kStep) {
-    if (t0 + kStep < v1) load(t0 + kStep, next);
-    float mt = VT::largest(raw[0]);
-#pragma unroll
-    for (int u = 1; u < kU; ++u) mt = max_nan(mt, VT::largest(raw[u]));
-    if (!(mt <= acc.m)) acc.raise(mt, c);
+    uint4 raw[kU];
+    load(t0, raw);
+    const float mt = VT::largest(raw);
+    if (!(mt <= acc.m)) acc.raise<false>(mt, c);
     {
-      const uint64_t nm2 = pack2(-acc.m, -acc.m);
+      const float r = __fmul_rn(acc.m, c);
+      const uint64_t nr2 = pack2(-r, -r);
       uint64_t z2 = pack2(acc.z, 0.f), s2 = pack2(acc.s, 0.f);
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
@@ -344,7 +352,7 @@ __global__ void __launch_bounds__(kNT, 3) logprobs_kernel(const LpParams p, int 
         VT::unpack_near(raw[u], x);
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
-          const uint64_t y2 = mul2(add2(pack2(x[i], x[i + 1]), nm2), c2);
+          const uint64_t y2 = fma2(pack2(x[i], x[i + 1]), c2, nr2);
           float ya, yb;
           unpack2(y2, ya, yb);
           const uint64_t e2 = pack2(ex2f(ya), ex2f(yb));
@@ -360,14 +368,13 @@ __global__ void __launch_bounds__(kNT, 3) logprobs_kernel(const LpParams p, int 
     }
     if (K > 0) {
       const float top = mt == mt ? mt : -INFINITY;
-      if (t0 == w0) {  // the K-th largest lane maximum (ties by lane)
-        int r = 0;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const float o = __shfl_sync(kFull, top, i);
-          r += o > top || (o == top && i < lane);
+      if (t0 == w0) {  // the K-th largest of the lanes' maxima, or a smaller one
+        uint32_t left = order_bits(top), kth_top = 0;
+        for (int r = 0; r < K; ++r) {
+          kth_top = __reduce_max_sync(kFull, left);
+          if (left == kth_top) left = 0;
         }
-        if (r == K - 1) atomicMax(&bound, order_bits(top));
+        if (lane == 0) atomicMax(&bound, kth_top);
         __syncwarp();
       }
       const float b = order_value(*(volatile uint32_t*)&bound);
@@ -392,6 +399,7 @@ __global__ void __launch_bounds__(kNT, 3) logprobs_kernel(const LpParams p, int 
             }
           }
         }
+        if (K == 1 && top > b) atomicMax(&bound, order_bits(top));
         __syncwarp();
         const int n = *(volatile int*)&counts[warp];
         if (n > kCut) {
@@ -432,42 +440,59 @@ __global__ void __launch_bounds__(kNT, 3) logprobs_kernel(const LpParams p, int 
         }
       }
     }
-#pragma unroll
-    for (int u = 0; u < kU; ++u) raw[u] = next[u];
   }
   if (K > 0) {
-    warp_cut(lists[warp], counts[warp], K);
-    if (lane < K) cand[warp * K + lane] = lists[warp][lane];
+    // what reaches the final bound; where that is more than fits (equal logits),
+    // each warp's K largest
     __syncthreads();
-    cut_down(cand, kWarps * K, K);
+    const int n = counts[warp];
+    for (int i = lane; i < n; i += 32) {
+      const uint64_t k = lists[warp][i];
+      if ((uint32_t)(k >> 32) >= bound) {
+        const int at = atomicAdd(&total, 1);
+        if (at < kNT) cand[at] = k;
+      }
+    }
+    __syncthreads();
+    int m = total;
+    if (m > kNT) {
+      warp_cut(lists[warp], n, K);
+      if (lane < K) cand[warp * K + lane] = lists[warp][lane];
+      m = kWarps * K;
+      __syncthreads();
+    }
+    cut_down(cand, m, K);
   }
 
   // join the threads' sums in part[]: lanes, then warps
-  auto join_cta = [&]() {
+  auto join_cta = [&](auto far) {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
       Sums o;
       o.m = __shfl_xor_sync(kFull, acc.m, d);
       o.z = __shfl_xor_sync(kFull, acc.z, d);
       o.s = __shfl_xor_sync(kFull, acc.s, d);
-      acc.join(o, c);
+      acc.join<far.value>(o, c);
     }
     if (lane == 0) { wm[warp] = acc.m; wz[warp] = acc.z; ws[warp] = acc.s; }
     __syncthreads();
-    if (tid == 0) {
+    if (warp == 0) {
       Sums a;
-      a.m = wm[0]; a.z = wz[0]; a.s = ws[0];
-      for (int w = 1; w < kWarps; ++w) {
+      a.m = wm[lane % kWarps]; a.z = wz[lane % kWarps]; a.s = ws[lane % kWarps];
+#pragma unroll
+      for (int d = kWarps / 2; d > 0; d >>= 1) {
         Sums o;
-        o.m = wm[w]; o.z = wz[w]; o.s = ws[w];
-        a.join(o, c);
+        o.m = __shfl_xor_sync(kFull, a.m, d);
+        o.z = __shfl_xor_sync(kFull, a.z, d);
+        o.s = __shfl_xor_sync(kFull, a.s, d);
+        a.join<far.value>(o, c);
       }
-      part[0] = a.m; part[1] = a.z; part[2] = a.s;
+      if (lane == 0) { part[0] = a.m; part[1] = a.z; part[2] = a.s; }
     }
     if (C > 1) cluster_sync_all();  // part[] (and cand[0, K)) of every CTA are in place
     else __syncthreads();
   };
-  join_cta();
+  join_cta(std::false_type{});
   float row_max = part[0];
   if (C > 1)
     for (int r = 0; r < C; ++r) row_max = max_nan(row_max, remote_f32(&part[0], r));
@@ -477,12 +502,15 @@ __global__ void __launch_bounds__(kNT, 3) logprobs_kernel(const LpParams p, int 
     acc.z = acc.s = 0.f;
     for (int t0 = w0; t0 < v1; t0 += kStep)
       each_again(t0, [&](float x, int) {
-        if (x > acc.m) acc.raise(x, c);
-        acc.add(x, c);
+        if (x > acc.m) acc.raise<true>(x, c);
+        const float y = max_nan((x - acc.m) * c, kFloor);
+        const float e = ex2f(y);
+        acc.z += e;
+        acc.s = fmaf(e, y, acc.s);
       });
     if (C > 1) cluster_sync_all();  // the first sums have been read everywhere
     else __syncthreads();
-    join_cta();
+    join_cta(std::true_type{});
   }
   if (C > 1) {
     if (rank == 0) {
@@ -494,7 +522,8 @@ __global__ void __launch_bounds__(kNT, 3) logprobs_kernel(const LpParams p, int 
           o.m = remote_f32(&part[0], r);
           o.z = remote_f32(&part[1], r);
           o.s = remote_f32(&part[2], r);
-          a.join(o, c);
+          if (far) a.join<true>(o, c);
+          else a.join<false>(o, c);
         }
         whole[0] = a.m; whole[1] = a.z; whole[2] = a.s;
       }
@@ -510,12 +539,13 @@ __global__ void __launch_bounds__(kNT, 3) logprobs_kernel(const LpParams p, int 
   if (tid == 0) {
     const float m = whole[0], z = whole[1];
     const bool bad = !(z == z) || !(m == m) || m == INFINITY;
-    const float lnz = logf(z);  // z = 0 (no finite logit): -inf
+    const float eps = far ? 0.f : fmaf(m, c, -__fmul_rn(m, c));
+    const float lnz = logf(z) - eps * kLn2;  // z = 0 (no finite logit): -inf
     fin[0] = m;
     fin[1] = bad ? NAN : lnz;
     if (p.lse) p.lse[row] = bad ? NAN : (z > 0.f ? fmaf(m, p.scale, lnz) : -INFINITY);
     if (p.entropy)
-      p.entropy[row] = bad ? NAN : (z > 0.f ? fmaxf(lnz - kLn2 * (whole[2] / z), 0.f) : 0.f);
+      p.entropy[row] = bad ? NAN : (z > 0.f ? fmaxf(logf(z) - kLn2 * (whole[2] / z), 0.f) : 0.f);
     if (bad && p.row_status) p.row_status[row] = VA_ERR_INVALID_ARG;
   }
   __syncthreads();
