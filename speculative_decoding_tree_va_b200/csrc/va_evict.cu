@@ -2,7 +2,10 @@
 // plan (which keys stay, in which slots) and the move of one cache's keys.
 //
 // Plan.  One cluster per request; CTA r of C owns a contiguous part of the
-// slots.  The k heaviest unprotected candidates are found by a radix select
+// slots and holds one key each in shared memory: 0 for a dropped slot, all ones
+// for a protected one, else order-preserving bits of the weight (those lie
+// strictly between).  Requests too long for that read their weights again in
+// every pass.  The k heaviest unprotected candidates are found by a radix select
 // on order-preserving bits of the weights (digits of 11, 11 and 10 bits; one
 // shared-memory histogram per CTA, joined over distributed shared memory),
 // ties by lower slot through each CTA's count of the last digit.  Kept slots
@@ -30,6 +33,8 @@ constexpr int kVec = 4;               // consecutive slots of a thread in a tile
 constexpr int kTile = kNT * kVec;
 constexpr int kBins = 2048;
 constexpr int kMaxKeepBytes = 128 * 1024;  // keep bits of a CTA's slots in shared memory
+constexpr int kMaxHeldBytes = 200 * 1024;  // keys and keep bits
+constexpr uint32_t kDropped = 0u, kProtected = ~0u;
 constexpr int kMaxCluster = 8;
 constexpr unsigned kFull = 0xffffffffu;
 
@@ -110,9 +115,22 @@ __device__ uint32_t block_scan(uint32_t v, Shared& s, uint32_t* total) {
   return before;
 }
 
+// Counts a digit per lane (kNoDigit: none); called by whole warps.
+constexpr uint32_t kNoDigit = ~0u;
+__device__ __forceinline__ void count_digit(uint32_t* hist, uint32_t digit) {
+  int same;
+  __match_all_sync(kFull, digit, &same);  // as with weights that are all zero
+  if (same) {
+    if ((threadIdx.x & 31) == 0 && digit != kNoDigit) atomicAdd(&hist[digit], 32u);
+  } else if (digit != kNoDigit) {
+    atomicAdd(&hist[digit], 1u);
+  }
+}
+
+template <bool Held>
 __global__ void __launch_bounds__(kNT) evict_plan_kernel(const PlanParams p, int C) {
   __shared__ Shared s;
-  extern __shared__ uint8_t keep4[];  // keep bits of this CTA's slots, one quad a byte
+  extern __shared__ uint32_t dyn[];  // keys of this CTA's slots (Held), then their keep bits
   const int tid = threadIdx.x, lane = tid & 31;
   const uint32_t rank = C > 1 ? cluster_rank() : 0;
   const int b = blockIdx.x / C;
@@ -158,6 +176,8 @@ __global__ void __launch_bounds__(kNT) evict_plan_kernel(const PlanParams p, int
   const int per = slots_per_cta(cap, C);
   const int lo = min(cap, (int)rank * per), hi = min(cap, lo + per);
   const int hiN = min(hi, max(lo, N));
+  uint32_t* held = dyn;
+  uint8_t* keep4 = reinterpret_cast<uint8_t*>(dyn + (Held ? per : 0));  // one quad a byte
 
   auto accepted = [&](int j) {
     const int n = j - P;
@@ -174,8 +194,11 @@ __global__ void __launch_bounds__(kNT) evict_plan_kernel(const PlanParams p, int
       newest = last;
     } else {
       int mine = INT_MIN;
-      for (int j = lo + tid; j < hiN; j += kNT)
-        if (j < P || accepted(j)) mine = max(mine, pos[j]);
+#pragma unroll 4
+      for (int j = lo + tid; j < hiN; j += kNT) {
+        const int q = pos[j];
+        if (j < P || accepted(j)) mine = max(mine, q);
+      }
       if (tid == 0) s.newest = INT_MIN;
       __syncthreads();
       mine = __reduce_max_sync(kFull, mine);
@@ -186,21 +209,26 @@ __global__ void __launch_bounds__(kNT) evict_plan_kernel(const PlanParams p, int
         for (int r = 0; r < C; ++r) newest = max(newest, (int)remote_u32(&s.newest, r));
     }
   }
-  // class of a slot: 0 dropped, 1 ranked by weight, 2 protected
-  auto group = [&](int j) {
-    if (j >= P) return accepted(j) ? 2 : 0;
+  auto make_key = [&](int j) -> uint32_t {
+    const float x = w[j];
     const int q = pos ? pos[j] : j;
-    if (q < p.n_sink || (p.n_recent > 0 && (long long)newest - q < p.n_recent)) return 2;
-    return 1;
+    const bool safe = q < p.n_sink || (p.n_recent > 0 && (long long)newest - q < p.n_recent);
+    if (j >= P) return accepted(j) ? kProtected : kDropped;
+    return safe ? kProtected : order_bits(x);
   };
+  auto key_of = [&](int j) { return Held ? held[j - lo] : make_key(j); };
+  auto ranked = [](uint32_t k) { return k != kDropped && k != kProtected; };
 
-  // protected keys, and the first digit's histogram
+  // the keys, how many are protected, and the first digit's histogram
   {
     uint32_t prot = 0;
-    for (int j = lo + tid; j < hiN; j += kNT) {
-      const int g = group(j);
-      prot += g == 2;
-      if (g == 1) atomicAdd(&s.hist[0][order_bits(w[j]) >> 21], 1u);
+#pragma unroll 4
+    for (int j0 = lo; j0 < hiN; j0 += kNT) {
+      const int j = j0 + tid;
+      const uint32_t k = j < hiN ? make_key(j) : kDropped;
+      if (Held && j < hiN) held[j - lo] = k;
+      prot += k == kProtected;
+      count_digit(s.hist[0], ranked(k) ? k >> 21 : kNoDigit);
     }
     prot = __reduce_add_sync(kFull, prot);
     if (lane == 0 && prot) atomicAdd(&s.cnt[0], prot);
@@ -227,10 +255,12 @@ __global__ void __launch_bounds__(kNT) evict_plan_kernel(const PlanParams p, int
       uint32_t* h = s.hist[pass & 1];
       if (pass > 0) {
         const int above = pass == 1 ? 21 : 10;
-        for (int j = lo + tid; j < hiN; j += kNT) {
-          if (group(j) != 1) continue;
-          const uint32_t o = order_bits(w[j]);
-          if ((o >> above) == (prefix >> above)) atomicAdd(&h[(o >> shift) & (bins - 1)], 1u);
+#pragma unroll 4
+        for (int j0 = lo; j0 < hiN; j0 += kNT) {
+          const int j = j0 + tid;
+          const uint32_t k = j < hiN ? key_of(j) : kDropped;
+          const bool in = ranked(k) && (k >> above) == (prefix >> above);
+          count_digit(h, in ? (k >> shift) & (bins - 1) : kNoDigit);
         }
         sync();
       }
@@ -280,15 +310,11 @@ __global__ void __launch_bounds__(kNT) evict_plan_kernel(const PlanParams p, int
       const int j = j0 + i;
       if (j >= hiN) continue;
       if (asis) { keep |= 1u << i; continue; }
-      const int g = group(j);
-      if (g == 2) keep |= 1u << i;
-      if (g == 1 && k > 0) {
-        if (!select) keep |= 1u << i;
-        else {
-          const uint32_t o = order_bits(w[j]);
-          if (o > key_lo) keep |= 1u << i;
-          if (o == key_lo) eq |= 1u << i;
-        }
+      const uint32_t o = key_of(j);
+      if (o == kProtected) keep |= 1u << i;
+      if (ranked(o) && k > 0) {
+        if (!select || o > key_lo) keep |= 1u << i;
+        else if (o == key_lo) eq |= 1u << i;
       }
     }
     if (select) {
@@ -389,11 +415,20 @@ __global__ void __launch_bounds__(kNT) evict_plan_kernel(const PlanParams p, int
 
 constexpr int kMoveThreads = 256;
 
+__device__ __forceinline__ uint4 load_once(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
+// E: bytes of an element.
+template <int E>
 __global__ void __launch_bounds__(kMoveThreads)
-kv_move_kernel(uint4* __restrict__ c_kv, uint4* __restrict__ k_pe, int cw, int kw, int num_pages,
-               const int32_t* __restrict__ table, int max_pages,
-               const int32_t* __restrict__ from_slot, const int32_t* __restrict__ new_len,
-               int32_t* __restrict__ req_status) {
+kv_move_kernel(uint4* c_kv, uint4* k_pe, int num_pages, const int32_t* __restrict__ table,
+               int max_pages, const int32_t* __restrict__ from_slot,
+               const int32_t* __restrict__ new_len, int32_t* __restrict__ req_status) {
+  constexpr int cw = kDc * E / 16, kw = kDr * E / 16;  // 16-byte words of a row
   __shared__ int2 move[kPage];  // pool rows: destination, source
   __shared__ int n_moves;
   const int b = blockIdx.y, page = blockIdx.x, tid = threadIdx.x;
@@ -422,12 +457,26 @@ kv_move_kernel(uint4* __restrict__ c_kv, uint4* __restrict__ k_pe, int cw, int k
     }
   }
   __syncthreads();
-  const int per = cw + kw, total = n_moves * per;
-  for (int i = tid; i < total; i += kMoveThreads) {
-    const int2 m = move[i / per];
-    const int x = i % per;
-    if (x < cw) c_kv[(size_t)m.x * cw + x] = c_kv[(size_t)m.y * cw + x];
-    else k_pe[(size_t)m.x * kw + x - cw] = k_pe[(size_t)m.y * kw + x - cw];
+  // kBatch words of each thread are in flight
+  constexpr int per = cw + kw, kBatch = 4;
+  const int total = n_moves * per;
+  for (int i0 = tid; i0 < total; i0 += kMoveThreads * kBatch) {
+    uint4 v[kBatch];
+    uint4* to[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int i = i0 + u * kMoveThreads;
+      to[u] = nullptr;
+      if (i < total) {
+        const int2 m = move[i / per];
+        const int x = i % per;
+        to[u] = x < cw ? c_kv + (size_t)m.x * cw + x : k_pe + (size_t)m.x * kw + (x - cw);
+        v[u] = load_once(x < cw ? c_kv + (size_t)m.y * cw + x : k_pe + (size_t)m.y * kw + (x - cw));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      if (to[u]) *to[u] = v[u];
   }
 }
 
@@ -457,11 +506,14 @@ cudaError_t launch_evict_plan(const va_evict_args& a, int sms, cudaStream_t st) 
          (((long long)a.B * C < sms && (long long)a.capacity > (long long)kTile * C) ||
           slots_per_cta(a.capacity, C) / kVec > kMaxKeepBytes))
     C *= 2;
-  const int keep_bytes = slots_per_cta(a.capacity, C) / kVec;
-  if (keep_bytes > kMaxKeepBytes) return cudaErrorNotSupported;
-  if (keep_bytes > 24 * 1024) {  // past the default limit; the same value from every thread
-    cudaError_t e = cudaFuncSetAttribute(
-        evict_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxKeepBytes);
+  const int slots = slots_per_cta(a.capacity, C);
+  if (slots / kVec > kMaxKeepBytes) return cudaErrorNotSupported;
+  const bool held = slots * 4 + slots / kVec <= kMaxHeldBytes;
+  const int bytes = (held ? slots * 4 : 0) + slots / kVec;
+  auto* kernel = held ? evict_plan_kernel<true> : evict_plan_kernel<false>;
+  if (bytes > 24 * 1024) {  // past the default limit; the same value from every thread
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         held ? kMaxHeldBytes : kMaxKeepBytes);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchAttribute at[1];
@@ -472,11 +524,11 @@ cudaError_t launch_evict_plan(const va_evict_args& a, int sms, cudaStream_t st) 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((long long)a.B * C));
   cfg.blockDim = dim3(kNT);
-  cfg.dynamicSmemBytes = keep_bytes;
+  cfg.dynamicSmemBytes = bytes;
   cfg.stream = st;
   cfg.attrs = at;
   cfg.numAttrs = C > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, evict_plan_kernel, p, C);
+  return cudaLaunchKernelEx(&cfg, kernel, p, C);
 }
 
 cudaError_t launch_kv_move(void* c_kv, void* k_pe, int elem_bytes, int num_pages,
@@ -484,9 +536,9 @@ cudaError_t launch_kv_move(void* c_kv, void* k_pe, int elem_bytes, int num_pages
                            const int32_t* from_slot, const int32_t* new_len, int32_t* req_status,
                            cudaStream_t st) {
   const dim3 grid((unsigned)max_pages, (unsigned)B);
-  kv_move_kernel<<<grid, kMoveThreads, 0, st>>>(
-      static_cast<uint4*>(c_kv), static_cast<uint4*>(k_pe), kDc * elem_bytes / 16,
-      kDr * elem_bytes / 16, num_pages, page_table, max_pages, from_slot, new_len, req_status);
+  auto* kernel = elem_bytes == 4 ? kv_move_kernel<4> : elem_bytes == 2 ? kv_move_kernel<2> : kv_move_kernel<1>;
+  kernel<<<grid, kMoveThreads, 0, st>>>(static_cast<uint4*>(c_kv), static_cast<uint4*>(k_pe), num_pages,
+                                        page_table, max_pages, from_slot, new_len, req_status);
   return cudaGetLastError();
 }
 
