@@ -33,7 +33,7 @@ constexpr int kVec = 4;               // consecutive slots of a thread in a tile
 constexpr int kTile = kNT * kVec;
 constexpr int kBins = 2048;
 constexpr int kMaxKeepBytes = 128 * 1024;  // keep bits of a CTA's slots in shared memory
-constexpr int kMaxHeldBytes = 200 * 1024;  // keys and keep bits
+constexpr int kMaxRun = 32;                // slots of a thread whose keys are held
 constexpr uint32_t kDropped = 0u, kProtected = ~0u;
 constexpr int kMaxCluster = 8;
 constexpr unsigned kFull = 0xffffffffu;
@@ -115,22 +115,10 @@ __device__ uint32_t block_scan(uint32_t v, Shared& s, uint32_t* total) {
   return before;
 }
 
-// Counts a digit per lane (kNoDigit: none); called by whole warps.
-constexpr uint32_t kNoDigit = ~0u;
-__device__ __forceinline__ void count_digit(uint32_t* hist, uint32_t digit) {
-  int same;
-  __match_all_sync(kFull, digit, &same);  // as with weights that are all zero
-  if (same) {
-    if ((threadIdx.x & 31) == 0 && digit != kNoDigit) atomicAdd(&hist[digit], 32u);
-  } else if (digit != kNoDigit) {
-    atomicAdd(&hist[digit], 1u);
-  }
-}
-
 template <bool Held>
 __global__ void __launch_bounds__(kNT) evict_plan_kernel(const PlanParams p, int C) {
   __shared__ Shared s;
-  extern __shared__ uint32_t dyn[];  // keys of this CTA's slots (Held), then their keep bits
+  extern __shared__ uint32_t dyn[];  // keys of this CTA's slots (Held) and their keep bits
   const int tid = threadIdx.x, lane = tid & 31;
   const uint32_t rank = C > 1 ? cluster_rank() : 0;
   const int b = blockIdx.x / C;
@@ -176,8 +164,10 @@ __global__ void __launch_bounds__(kNT) evict_plan_kernel(const PlanParams p, int
   const int per = slots_per_cta(cap, C);
   const int lo = min(cap, (int)rank * per), hi = min(cap, lo + per);
   const int hiN = min(hi, max(lo, N));
+  const int run = (per + kNT - 1) / kNT;  // Held: consecutive slots of a thread, at most 32
   uint32_t* held = dyn;
-  uint8_t* keep4 = reinterpret_cast<uint8_t*>(dyn + (Held ? per : 0));  // one quad a byte
+  uint32_t* kept = dyn + kNT * run;       // Held: then one bit per slot
+  uint8_t* keep4 = reinterpret_cast<uint8_t*>(dyn);  // else: one quad a byte
 
   auto accepted = [&](int j) {
     const int n = j - P;
@@ -209,12 +199,15 @@ __global__ void __launch_bounds__(kNT) evict_plan_kernel(const PlanParams p, int
         for (int r = 0; r < C; ++r) newest = max(newest, (int)remote_u32(&s.newest, r));
     }
   }
+  // positions from here on are recent
+  const int recent = p.n_recent > 0
+                         ? (int)max((long long)newest - p.n_recent + 1, (long long)INT_MIN)
+                         : INT_MAX;
   auto make_key = [&](int j) -> uint32_t {
     const float x = w[j];
     const int q = pos ? pos[j] : j;
-    const bool safe = q < p.n_sink || (p.n_recent > 0 && (long long)newest - q < p.n_recent);
     if (j >= P) return accepted(j) ? kProtected : kDropped;
-    return safe ? kProtected : order_bits(x);
+    return q < p.n_sink || (q >= recent && p.n_recent > 0) ? kProtected : order_bits(x);
   };
   auto key_of = [&](int j) { return Held ? held[j - lo] : make_key(j); };
   auto ranked = [](uint32_t k) { return k != kDropped && k != kProtected; };
@@ -223,13 +216,14 @@ __global__ void __launch_bounds__(kNT) evict_plan_kernel(const PlanParams p, int
   {
     uint32_t prot = 0;
 #pragma unroll 4
-    for (int j0 = lo; j0 < hiN; j0 += kNT) {
-      const int j = j0 + tid;
-      const uint32_t k = j < hiN ? make_key(j) : kDropped;
-      if (Held && j < hiN) held[j - lo] = k;
+    for (int j = lo + tid; j < hiN; j += kNT) {
+      const uint32_t k = make_key(j);
+      if (Held) held[j - lo] = k;
       prot += k == kProtected;
-      count_digit(s.hist[0], ranked(k) ? k >> 21 : kNoDigit);
+      if (ranked(k)) atomicAdd(&s.hist[0][k >> 21], 1u);
     }
+    if (Held)  // slots behind the last key, to the end of the threads' runs
+      for (int j = max(hiN, lo) + tid; j < lo + kNT * run; j += kNT) held[j - lo] = kDropped;
     prot = __reduce_add_sync(kFull, prot);
     if (lane == 0 && prot) atomicAdd(&s.cnt[0], prot);
   }
@@ -256,11 +250,10 @@ __global__ void __launch_bounds__(kNT) evict_plan_kernel(const PlanParams p, int
       if (pass > 0) {
         const int above = pass == 1 ? 21 : 10;
 #pragma unroll 4
-        for (int j0 = lo; j0 < hiN; j0 += kNT) {
-          const int j = j0 + tid;
-          const uint32_t k = j < hiN ? key_of(j) : kDropped;
-          const bool in = ranked(k) && (k >> above) == (prefix >> above);
-          count_digit(h, in ? (k >> shift) & (bins - 1) : kNoDigit);
+        for (int j = lo + tid; j < hiN; j += kNT) {
+          const uint32_t k = key_of(j);
+          if (ranked(k) && (k >> above) == (prefix >> above))
+            atomicAdd(&h[(k >> shift) & (bins - 1)], 1u);
         }
         sync();
       }
@@ -299,6 +292,75 @@ __global__ void __launch_bounds__(kNT) evict_plan_kernel(const PlanParams p, int
     }
   }
   const uint32_t key_lo = prefix;
+
+  if constexpr (Held) {
+    // Each thread takes the run of slots [j0, j0 + run): which of them stay, ...
+    const int j0 = lo + tid * run;
+    uint32_t keep = 0, eq = 0, total;
+    for (int i = 0; i < run; ++i) {
+      const uint32_t o = held[tid * run + i];
+      const bool in = asis ? j0 + i < hiN
+                           : o == kProtected || (ranked(o) && k > 0 && (!select || o > key_lo));
+      if (in) keep |= 1u << i;
+      else if (select && o == key_lo) eq |= 1u << i;
+    }
+    if (select) {  // ... ties by lower slot
+      uint32_t at = ties_before + block_scan(__popc(eq), s, &total);
+      for (; eq && at < need; ++at) {
+        keep |= eq & (0u - eq);
+        eq &= eq - 1;
+      }
+    }
+    const int in_run = min(max(hi - j0, 0), run), below_n = min(max(n_new - j0, 0), in_run);
+    const uint32_t below = below_n >= 32 ? ~0u : (1u << below_n) - 1u;
+    uint32_t hole = ~keep & below, mover = keep & ~below;
+    // Indices of its holes and movers: the CTA's (at most 32768 each) in one scan,
+    // then the cluster's.  The outputs may overwrite the inputs from here on.
+    const uint32_t both = block_scan(__popc(hole) | __popc(mover) << 16, s, &total);
+    if (tid == 0) { s.cnt[2] = total & 0xffffu; s.cnt[3] = total >> 16; }
+    for (int i = tid; i < (kNT * run + 31) / 32; i += kNT) kept[i] = 0;
+    sync();
+    {  // the run's bits, in one or two words
+      const int bit = tid * run, sh = bit & 31;
+      if (keep) atomicOr(&kept[bit >> 5], keep << sh);
+      if (sh && keep >> (32 - sh)) atomicOr(&kept[(bit >> 5) + 1], keep >> (32 - sh));
+    }
+    uint32_t hole_at = both & 0xffffu, mover_at = both >> 16;
+    for (int r = 0; r < (int)rank; ++r) {
+      hole_at += remote_u32(&s.cnt[2], r);
+      mover_at += remote_u32(&s.cnt[3], r);
+    }
+    // list the holes in from_slot[n_new ..): there are as many as movers, which
+    // all lie there, so the list fits
+    for (; hole; hole &= hole - 1)
+      p.from_slot[row + n_new + hole_at++] = j0 + __ffs(hole) - 1;
+    __threadfence();
+    sync();
+    // a mover's key goes to its hole, the other kept slots keep theirs
+    for (; mover; mover &= mover - 1) {
+      const int j = j0 + __ffs(mover) - 1;
+      const int to = __ldcg(&p.from_slot[row + n_new + mover_at++]);
+      p.from_slot[row + to] = j;
+      if (p.weights_out) p.weights_out[row + to] = w[j];
+      if (p.pos_out) p.pos_out[row + to] = pos[j];
+    }
+#pragma unroll 4
+    for (int j = lo + tid; j < min(hi, n_new); j += kNT) {
+      if (!((kept[(j - lo) >> 5] >> ((j - lo) & 31)) & 1u)) continue;
+      p.from_slot[row + j] = j;
+      if (p.weights_out) p.weights_out[row + j] = w[j];
+      if (p.pos_out) p.pos_out[row + j] = pos[j];
+    }
+    sync();
+#pragma unroll 4
+    for (int j = max(lo, n_new) + tid; j < hi; j += kNT) {
+      p.from_slot[row + j] = -1;
+      if (p.weights_out) p.weights_out[row + j] = 0.f;
+      if (p.pos_out) p.pos_out[row + j] = -1;
+    }
+    if (rank == 0 && tid == 0) p.new_len[b] = n_new;
+    return;
+  }
 
   // One tile: which of this thread's slots stay.  `tie` counts the ties seen
   // in earlier tiles (same value in every thread).
@@ -508,12 +570,13 @@ cudaError_t launch_evict_plan(const va_evict_args& a, int sms, cudaStream_t st) 
     C *= 2;
   const int slots = slots_per_cta(a.capacity, C);
   if (slots / kVec > kMaxKeepBytes) return cudaErrorNotSupported;
-  const bool held = slots * 4 + slots / kVec <= kMaxHeldBytes;
-  const int bytes = (held ? slots * 4 : 0) + slots / kVec;
+  const int run = (slots + kNT - 1) / kNT;
+  const bool held = run <= kMaxRun;
+  const int bytes = held ? kNT * run * 4 + kNT * run / 8 + 4 : slots / kVec;
   auto* kernel = held ? evict_plan_kernel<true> : evict_plan_kernel<false>;
   if (bytes > 24 * 1024) {  // past the default limit; the same value from every thread
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         held ? kMaxHeldBytes : kMaxKeepBytes);
+                                         held ? kNT * kMaxRun * 4 + kNT * kMaxRun / 8 + 4 : kMaxKeepBytes);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchAttribute at[1];

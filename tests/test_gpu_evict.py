@@ -67,6 +67,17 @@ def test_plans(va, B, cap, T, sink, recent, pos, in_place):
                    what=f"cap {cap} share {share}")
 
 
+@pytest.mark.parametrize("cap", [262144, 262145, 300003])
+def test_longest_requests(va, cap):
+    """Around the length whose keys no longer fit in the cluster's shared memory."""
+    rng = np.random.default_rng(cap)
+    w, kv_len, path, alen = make(rng, 1, cap, 33)
+    w[0, ::3] = 1.0
+    at = rng.permutation(2 * cap)[:cap].astype(np.int32)[None]
+    check_plan(va, w, kv_len, np.array([cap // 3 + 5], np.int32), 33, path, alen, at, 7, 1000,
+               in_place=True, what=f"cap {cap}")
+
+
 def test_ties_and_special_weights(va):
     """Equal weights go by slot; NaN ranks like -inf; +-0 are equal; infinities rank."""
     rng = np.random.default_rng(8)
