@@ -32,6 +32,7 @@ constexpr int kNT = 1024;
 constexpr int kVec = 4;               // consecutive slots of a thread in a tile
 constexpr int kTile = kNT * kVec;
 constexpr int kBins = 2048;
+constexpr int kBatch = 8;             // loads of a thread in flight
 constexpr int kMaxKeepBytes = 128 * 1024;  // keep bits of a CTA's slots in shared memory
 constexpr int kMaxRun = 32;                // slots of a thread whose keys are held
 constexpr uint32_t kDropped = 0u, kProtected = ~0u;
@@ -70,6 +71,23 @@ __device__ __forceinline__ uint32_t remote_u32(const void* p, uint32_t rank) {
   asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
 }
+__device__ __forceinline__ uint2 remote_u32x2(const void* p, uint32_t rank) {
+  uint32_t a;
+  uint2 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
+  return v;
+}
+// Sum of *p over CTAs [0, n) of the cluster; the loads are independent.
+__device__ __forceinline__ uint32_t remote_sum(const uint32_t* p, int n) {
+  uint32_t v[kMaxCluster], sum = 0;
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r) v[r] = r < n ? remote_u32(p, r) : 0;
+#pragma unroll
+  for (int r = 0; r < kMaxCluster; ++r) sum += v[r];
+  return sum;
+}
 // Bits that order like the weight: -0 like +0, NaN like -inf.
 __device__ __forceinline__ uint32_t order_bits(float x) {
   if (!(x == x)) x = -INFINITY;
@@ -78,7 +96,7 @@ __device__ __forceinline__ uint32_t order_bits(float x) {
 }
 
 struct Shared {
-  uint32_t hist[2][kBins];
+  __align__(8) uint32_t hist[2][kBins];
   uint32_t warp_sum[32];
   uint32_t total;
   int32_t newest;                 // of this CTA
@@ -184,10 +202,22 @@ __global__ void __launch_bounds__(kNT) evict_plan_kernel(const PlanParams p, int
       newest = last;
     } else {
       int mine = INT_MIN;
-#pragma unroll 4
-      for (int j = lo + tid; j < hiN; j += kNT) {
-        const int q = pos[j];
-        if (j < P || accepted(j)) mine = max(mine, q);
+      for (int j0 = lo + tid; j0 < hiN; j0 += kNT * kBatch) {
+        int q[kBatch];
+        float x[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const int j = j0 + u * kNT;
+          q[u] = j < hiN ? pos[j] : INT_MIN;
+          if (Held) x[u] = j < hiN ? w[j] : 0.f;  // in the same wait
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+          const int j = j0 + u * kNT;
+          if (j >= hiN) break;
+          if (j < P || accepted(j)) mine = max(mine, q[u]);
+          if (Held) held[j - lo] = order_bits(x[u]);
+        }
       }
       if (tid == 0) s.newest = INT_MIN;
       __syncthreads();
@@ -195,32 +225,50 @@ __global__ void __launch_bounds__(kNT) evict_plan_kernel(const PlanParams p, int
       if (lane == 0) atomicMax(&s.newest, mine);
       sync();
       newest = s.newest;
-      if (C > 1)
-        for (int r = 0; r < C; ++r) newest = max(newest, (int)remote_u32(&s.newest, r));
+      if (C > 1) {
+        int v[kMaxCluster];
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) v[r] = r < C ? (int)remote_u32(&s.newest, r) : INT_MIN;
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) newest = max(newest, v[r]);
+      }
     }
   }
   // positions from here on are recent
   const int recent = p.n_recent > 0
                          ? (int)max((long long)newest - p.n_recent + 1, (long long)INT_MIN)
                          : INT_MAX;
-  auto make_key = [&](int j) -> uint32_t {
-    const float x = w[j];
-    const int q = pos ? pos[j] : j;
+  auto key_from = [&](int j, uint32_t bits, int q) -> uint32_t {
     if (j >= P) return accepted(j) ? kProtected : kDropped;
-    return q < p.n_sink || (q >= recent && p.n_recent > 0) ? kProtected : order_bits(x);
+    return q < p.n_sink || (q >= recent && p.n_recent > 0) ? kProtected : bits;
   };
-  auto key_of = [&](int j) { return Held ? held[j - lo] : make_key(j); };
+  auto key_of = [&](int j) {
+    return Held ? held[j - lo] : key_from(j, order_bits(w[j]), pos ? pos[j] : j);
+  };
   auto ranked = [](uint32_t k) { return k != kDropped && k != kProtected; };
 
   // the keys, how many are protected, and the first digit's histogram
   {
     uint32_t prot = 0;
-#pragma unroll 4
-    for (int j = lo + tid; j < hiN; j += kNT) {
-      const uint32_t k = make_key(j);
-      if (Held) held[j - lo] = k;
-      prot += k == kProtected;
-      if (ranked(k)) atomicAdd(&s.hist[0][k >> 21], 1u);
+    const bool have_bits = Held && pos && p.n_recent > 0;  // with the positions, above
+    for (int j0 = lo + tid; j0 < hiN; j0 += kNT * kBatch) {
+      int q[kBatch];
+      uint32_t bits[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int j = j0 + u * kNT;
+        q[u] = pos && j < hiN ? pos[j] : j;
+        bits[u] = j >= hiN ? 0u : have_bits ? held[j - lo] : order_bits(w[j]);
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int j = j0 + u * kNT;
+        if (j >= hiN) break;
+        const uint32_t k = key_from(j, bits[u], q[u]);
+        if (Held) held[j - lo] = k;
+        prot += k == kProtected;
+        if (ranked(k)) atomicAdd(&s.hist[0][k >> 21], 1u);
+      }
     }
     if (Held)  // slots behind the last key, to the end of the threads' runs
       for (int j = max(hiN, lo) + tid; j < lo + kNT * run; j += kNT) held[j - lo] = kDropped;
@@ -229,10 +277,7 @@ __global__ void __launch_bounds__(kNT) evict_plan_kernel(const PlanParams p, int
   }
   sync();
   uint32_t n_prot = s.cnt[0];
-  if (C > 1) {
-    n_prot = 0;
-    for (int r = 0; r < C; ++r) n_prot += remote_u32(&s.cnt[0], r);
-  }
+  if (C > 1) n_prot = remote_sum(&s.cnt[0], C);
   const int n_cand = P + n_acc;
   const int n_other = n_cand - (int)n_prot;
   const int n_new = asis ? N : max(min(max(p.budget[b], 0), n_cand), (int)n_prot);
@@ -262,9 +307,14 @@ __global__ void __launch_bounds__(kNT) evict_plan_kernel(const PlanParams p, int
       const int d0 = bins - 1 - 2 * tid;
       if (d0 > 0) {
         if (C > 1) {
-          for (int r = 0; r < C; ++r) {
-            c0 += remote_u32(&h[d0], r);
-            c1 += remote_u32(&h[d0 - 1], r);
+          uint2 v[kMaxCluster];
+#pragma unroll
+          for (int r = 0; r < kMaxCluster; ++r)
+            v[r] = r < C ? remote_u32x2(&h[d0 - 1], r) : make_uint2(0, 0);
+#pragma unroll
+          for (int r = 0; r < kMaxCluster; ++r) {
+            c0 += v[r].y;
+            c1 += v[r].x;
           }
         } else {
           c0 = h[d0];
@@ -286,7 +336,7 @@ __global__ void __launch_bounds__(kNT) evict_plan_kernel(const PlanParams p, int
       need -= s.pick[1];
       if (pass == 2) {
         const uint32_t digit = prefix & 1023u;
-        for (int r = 0; r < (int)rank; ++r) ties_before += remote_u32(&h[digit], r);
+        ties_before = remote_sum(&h[digit], (int)rank);
       }
       __syncthreads();
     }
@@ -325,11 +375,8 @@ __global__ void __launch_bounds__(kNT) evict_plan_kernel(const PlanParams p, int
       if (keep) atomicOr(&kept[bit >> 5], keep << sh);
       if (sh && keep >> (32 - sh)) atomicOr(&kept[(bit >> 5) + 1], keep >> (32 - sh));
     }
-    uint32_t hole_at = both & 0xffffu, mover_at = both >> 16;
-    for (int r = 0; r < (int)rank; ++r) {
-      hole_at += remote_u32(&s.cnt[2], r);
-      mover_at += remote_u32(&s.cnt[3], r);
-    }
+    uint32_t hole_at = (both & 0xffffu) + remote_sum(&s.cnt[2], (int)rank);
+    uint32_t mover_at = (both >> 16) + remote_sum(&s.cnt[3], (int)rank);
     // list the holes in from_slot[n_new ..): there are as many as movers, which
     // all lie there, so the list fits
     for (; hole; hole &= hole - 1)
@@ -337,12 +384,26 @@ __global__ void __launch_bounds__(kNT) evict_plan_kernel(const PlanParams p, int
     __threadfence();
     sync();
     // a mover's key goes to its hole, the other kept slots keep theirs
-    for (; mover; mover &= mover - 1) {
-      const int j = j0 + __ffs(mover) - 1;
-      const int to = __ldcg(&p.from_slot[row + n_new + mover_at++]);
-      p.from_slot[row + to] = j;
-      if (p.weights_out) p.weights_out[row + to] = w[j];
-      if (p.pos_out) p.pos_out[row + to] = pos[j];
+    while (mover) {
+      constexpr int kFew = 4;
+      int j[kFew], to[kFew], q[kFew];
+      float x[kFew];
+#pragma unroll
+      for (int u = 0; u < kFew; ++u) {
+        j[u] = mover ? j0 + __ffs(mover) - 1 : -1;
+        if (j[u] < 0) continue;
+        mover &= mover - 1;
+        to[u] = __ldcg(&p.from_slot[row + n_new + mover_at++]);
+        if (p.weights_out) x[u] = w[j[u]];
+        if (p.pos_out) q[u] = pos[j[u]];
+      }
+#pragma unroll
+      for (int u = 0; u < kFew; ++u) {
+        if (j[u] < 0) continue;
+        p.from_slot[row + to[u]] = j[u];
+        if (p.weights_out) p.weights_out[row + to[u]] = x[u];
+        if (p.pos_out) p.pos_out[row + to[u]] = q[u];
+      }
     }
 #pragma unroll 4
     for (int j = lo + tid; j < min(hi, n_new); j += kNT) {
@@ -419,11 +480,8 @@ __global__ void __launch_bounds__(kNT) evict_plan_kernel(const PlanParams p, int
     if (lane == 0 && movers) atomicAdd(&s.cnt[3], movers);
   }
   sync();
-  uint32_t hole_at = 0, mover_at = 0;
-  for (int r = 0; r < (int)rank; ++r) {
-    hole_at += remote_u32(&s.cnt[2], r);
-    mover_at += remote_u32(&s.cnt[3], r);
-  }
+  const uint32_t hole_at = remote_sum(&s.cnt[2], (int)rank);
+  const uint32_t mover_at = remote_sum(&s.cnt[3], (int)rank);
   // list the holes in from_slot[n_new ..): there are as many as movers, which
   // all lie there, so the list fits
   {
@@ -519,14 +577,14 @@ kv_move_kernel(uint4* c_kv, uint4* k_pe, int num_pages, const int32_t* __restric
     }
   }
   __syncthreads();
-  // kBatch words of each thread are in flight
-  constexpr int per = cw + kw, kBatch = 4;
+  // kWords words of each thread are in flight
+  constexpr int per = cw + kw, kWords = 4;
   const int total = n_moves * per;
-  for (int i0 = tid; i0 < total; i0 += kMoveThreads * kBatch) {
-    uint4 v[kBatch];
-    uint4* to[kBatch];
+  for (int i0 = tid; i0 < total; i0 += kMoveThreads * kWords) {
+    uint4 v[kWords];
+    uint4* to[kWords];
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u) {
+    for (int u = 0; u < kWords; ++u) {
       const int i = i0 + u * kMoveThreads;
       to[u] = nullptr;
       if (i < total) {
@@ -537,7 +595,7 @@ kv_move_kernel(uint4* c_kv, uint4* k_pe, int num_pages, const int32_t* __restric
       }
     }
 #pragma unroll
-    for (int u = 0; u < kBatch; ++u)
+    for (int u = 0; u < kWords; ++u)
       if (to[u]) *to[u] = v[u];
   }
 }
@@ -561,11 +619,11 @@ cudaError_t launch_evict_plan(const va_evict_args& a, int sms, cudaStream_t st) 
   p.weights_out = a.weights_out;
   p.pos_out = a.pos ? a.pos_out : nullptr;
   p.req_status = a.req_status;
-  // A request is cut over a cluster while its CTAs keep more than a tile each
-  // and the SMs are not yet covered, or their keep bits would not fit.
+  // A request is cut over a cluster while its CTAs (one an SM) keep more than a
+  // tile each and there are SMs for them, or while their keep bits would not fit.
   int C = 1;
   while (C < kMaxCluster &&
-         (((long long)a.B * C < sms && (long long)a.capacity > (long long)kTile * C) ||
+         ((2LL * a.B * C <= sms && (long long)a.capacity > (long long)kTile * C) ||
           slots_per_cta(a.capacity, C) / kVec > kMaxKeepBytes))
     C *= 2;
   const int slots = slots_per_cta(a.capacity, C);
