@@ -335,26 +335,35 @@ def merge(o_part, lse_part, out_dtype, stream=None):
 # library checks the rest.  What they allocate belongs to the stream that
 # they run on.
 
+_NOWHERE = nullcontext()
+
+
 def _on(t, stream):
     """Context in which t's device and the given stream are the current ones."""
     import torch
-    if stream is None and t.device.index == torch.cuda.current_device():
-        return nullcontext()
+    if stream is None and t.get_device() == torch.cuda.current_device():
+        return _NOWHERE
+    if stream is not None and stream.device != t.device:
+        raise VerifyAttnError(f"stream of {stream.device} for tensors on {t.device}")
     ctx = ExitStack()
     ctx.enter_context(torch.cuda.device(t.device))
     if stream is not None:
-        if stream.device != t.device:
-            raise VerifyAttnError(f"stream of {stream.device} for tensors on {t.device}")
         ctx.enter_context(torch.cuda.stream(stream))
     return ctx
 
 
-def _need(t, name: str, like, dtypes, shape):
-    """One tensor argument: cuda, on like's device, one of dtypes, dense, of this shape."""
-    if t.device != like.device or t.device.type != "cuda":
+def _raw_stream(dev: int) -> int:
+    """Handle of the current stream of a device."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _need(t, name: str, dev: int, dtype, shape) -> int:
+    """Address of one tensor argument: on cuda device `dev`, of this type and shape, dense."""
+    if t.get_device() != dev or dev < 0:
         raise VerifyAttnError(f"{name} is on {t.device}: cuda tensors of one device are needed")
-    if t.dtype not in dtypes:
-        raise VerifyAttnError(f"{name} is {t.dtype}, not {' or '.join(str(d) for d in dtypes)}")
+    if t.dtype is not dtype:
+        raise VerifyAttnError(f"{name} is {t.dtype}, not {dtype}")
     if t.shape != shape:
         raise VerifyAttnError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
     if not t.is_contiguous():
@@ -384,53 +393,58 @@ def token_logprobs(logits, tokens=None, *, k: int = 0, scale: float = 1.0, wide:
     ``tree_accept(parents, tokens, r.top_ids[..., 0])`` for target logits [B, T, V]
     with k = 1."""
     import torch
-    if logits.device.type != "cuda":
+    dev, f32, i32 = logits.get_device(), torch.float32, torch.int32
+    if dev < 0:
         raise VerifyAttnError(f"logits are on {logits.device}: cuda tensors are needed")
-    if logits.dtype not in (torch.float32, torch.bfloat16):
+    if logits.dtype is not f32 and logits.dtype is not torch.bfloat16:
         raise VerifyAttnError(f"logits are {logits.dtype}, not float32 or bfloat16")
     if logits.dim() < 1 or logits.shape[-1] < 1:
         raise VerifyAttnError("logits need a vocabulary axis")
+    k = int(k)
+    if not 0 <= k <= 16:
+        raise VerifyAttnError("k is not in 0 .. 16")
     lead, V = logits.shape[:-1], logits.shape[-1]
     R = lead.numel()
     a = VaLogprobArgs()
+    a.ld = V
     if R:
-        try:
-            rows = logits.view(R, V)
-        except RuntimeError:
-            raise VerifyAttnError("logits rows are not evenly spaced") from None
-        if V > 1 and rows.stride(1) != 1:
+        rows = logits
+        if logits.dim() != 2:
+            try:
+                rows = logits.view(R, V)
+            except RuntimeError:
+                raise VerifyAttnError("logits rows are not evenly spaced") from None
+        ld, step = rows.stride()
+        if V > 1 and step != 1:
             raise VerifyAttnError("logits rows are not dense")
-        a.ld = rows.stride(0) if R > 1 else V
+        if R > 1:
+            a.ld = ld
         a.logits = logits.data_ptr()
-    else:
-        a.ld = V
-    a.dtype = VA_F32 if logits.dtype == torch.float32 else VA_BF16
-    a.R, a.V, a.K, a.scale = R, V, int(k), float(scale)
-    if not 0 <= a.K <= 16:
-        raise VerifyAttnError("k is not in 0 .. 16")
+    a.dtype = VA_F32 if logits.dtype is f32 else VA_BF16
+    a.R, a.V, a.K, a.scale = R, V, k, float(scale)
     with _on(logits, stream):
-        f32 = dict(device=logits.device, dtype=torch.float32)
-        lse, entropy = torch.empty(lead, **f32), torch.empty(lead, **f32)
+        lse = torch.empty(lead, device=logits.device, dtype=f32)
+        entropy = torch.empty_like(lse)
         a.lse, a.entropy = lse.data_ptr(), entropy.data_ptr()
         tok_lp = top_ids = top_lp = None
         if tokens is not None:
             G = 1 if tokens.shape == lead else tokens.shape[-1] if tokens.dim() else 0
-            want = lead if tokens.shape == lead else lead + (G,)
-            a.tokens, a.G = _need(tokens, "tokens", logits, (torch.int32,), want), G
-            tok_lp = torch.empty(tokens.shape, **f32)
+            a.tokens = _need(tokens, "tokens", dev, i32, lead if tokens.shape == lead else lead + (G,))
+            a.G = G
+            tok_lp = torch.empty_like(tokens, dtype=f32)
             a.tok_lp = tok_lp.data_ptr()
-        if a.K:
-            top_ids = torch.empty(lead + (a.K,), device=logits.device, dtype=torch.int32)
-            top_lp = torch.empty(lead + (a.K,), device=logits.device,
-                                 dtype=torch.float64 if wide else torch.float32)
+        if k:
+            top_ids = torch.empty(lead + (k,), device=logits.device, dtype=i32)
+            top_lp = torch.empty_like(top_ids, dtype=torch.float64 if wide else f32)
             a.top_ids = top_ids.data_ptr()
             if wide:
                 a.top_lp64 = top_lp.data_ptr()
             else:
                 a.top_lp = top_lp.data_ptr()
         if row_status is not None:
-            a.row_status = _need(row_status, "row_status", logits, (torch.int32,), lead)
-        _check(load_library().va_token_logprobs(ctypes.byref(a), _stream()), "va_token_logprobs")
+            a.row_status = _need(row_status, "row_status", dev, i32, lead)
+        _check(load_library().va_token_logprobs(ctypes.byref(a), _raw_stream(dev)),
+               "va_token_logprobs")
     return TokenLogprobs(lse, entropy, tok_lp, top_ids, top_lp)
 
 
@@ -449,47 +463,49 @@ def key_weights(q_nope, q_pe, c_kv, k_pe, page_table, kv_len, tree_mask, lse, *,
     if q_nope.dim() != 4:
         raise VerifyAttnError("q_nope is not [B, T, H, 512]")
     B, T, H, _ = q_nope.shape
-    i32, f32 = (torch.int32,), (torch.float32,)
-    qd = (torch.float32, torch.bfloat16)
+    dev, dt, i32, f32 = q_nope.get_device(), q_nope.dtype, torch.int32, torch.float32
+    if dt is not f32 and dt is not torch.bfloat16:
+        raise VerifyAttnError(f"q_nope is {dt}, not float32 or bfloat16")
     a = VaKeyWeightArgs()
-    a.q_nope = _need(q_nope, "q_nope", q_nope, qd, (B, T, H, D_LATENT))
-    a.q_pe = _need(q_pe, "q_pe", q_nope, (q_nope.dtype,), (B, T, H, D_ROPE))
+    a.q_nope = _need(q_nope, "q_nope", dev, dt, (B, T, H, D_LATENT))
+    a.q_pe = _need(q_pe, "q_pe", dev, dt, (B, T, H, D_ROPE))
     fp8 = _fp8_cache(c_kv)
-    kd = (c_kv.dtype,) if fp8 else (q_nope.dtype,)
-    n = c_kv.shape[0]
-    a.c_kv = _need(c_kv, "c_kv", q_nope, kd, (n, PAGE_SIZE, D_LATENT))
-    a.k_pe = _need(k_pe, "k_pe", q_nope, kd, (n, PAGE_SIZE, D_ROPE))
-    m = page_table.shape[-1]
-    a.page_table = _need(page_table, "page_table", q_nope, i32, (B, m))
-    a.kv_len = _need(kv_len, "kv_len", q_nope, i32, (B,))
-    a.tree_mask = _need(tree_mask, "tree_mask", q_nope, (torch.int64,), (B, T, (T + 63) // 64))
-    a.lse = _need(lse, "lse", q_nope, f32, (B, T, H))
+    kd = c_kv.dtype if fp8 else dt
+    n, m = c_kv.shape[0], page_table.shape[-1]
+    a.c_kv = _need(c_kv, "c_kv", dev, kd, (n, PAGE_SIZE, D_LATENT))
+    a.k_pe = _need(k_pe, "k_pe", dev, kd, (n, PAGE_SIZE, D_ROPE))
+    a.page_table = _need(page_table, "page_table", dev, i32, (B, m))
+    a.kv_len = _need(kv_len, "kv_len", dev, i32, (B,))
+    a.tree_mask = _need(tree_mask, "tree_mask", dev, torch.int64, (B, T, (T + 63) // 64))
+    a.lse = _need(lse, "lse", dev, f32, (B, T, H))
     if path is not None:
-        a.path = _need(path, "path", q_nope, i32, (B, T))
+        a.path = _need(path, "path", dev, i32, (B, T))
     if accept_len is not None:
-        a.accept_len = _need(accept_len, "accept_len", q_nope, i32, (B,))
+        a.accept_len = _need(accept_len, "accept_len", dev, i32, (B,))
     cap = (B, m * PAGE_SIZE)
     if weights is not None:
-        a.weights_in = _need(weights, "weights", q_nope, f32, cap)
+        a.weights_in = _need(weights, "weights", dev, f32, cap)
     if req_status is not None:
-        a.req_status = _need(req_status, "req_status", q_nope, i32, (B,))
-    a.dtype = VA_F32 if q_nope.dtype == torch.float32 else VA_BF16
+        a.req_status = _need(req_status, "req_status", dev, i32, (B,))
+    a.dtype = VA_F32 if dt is f32 else VA_BF16
     a.B, a.H, a.T, a.scale, a.decay = B, H, T, float(scale), float(decay)
     a.num_pages, a.page_size, a.max_pages = n, PAGE_SIZE, m
     a.flags = flags | (VA_FLAG_KV_FP8_E4M3 if fp8 else 0)
     a.kv_scale = float(kv_scale)
     with _on(q_nope, stream):
         if out is None:
-            out = torch.zeros(cap, device=q_nope.device, dtype=torch.float32)
-        a.weights = _need(out, "out", q_nope, f32, cap)
-        lib = load_library()
-        need = lib.va_key_weights_workspace_bytes(ctypes.byref(a))
+            out = torch.zeros(cap, device=q_nope.device, dtype=f32)
+        a.weights = _need(out, "out", dev, f32, cap)
+        lib, ref = load_library(), ctypes.byref(a)
+        need = lib.va_key_weights_workspace_bytes(ref)
         if need and workspace is None:
             workspace = torch.empty(need, device=q_nope.device, dtype=torch.uint8)
         if workspace is not None:
+            if workspace.get_device() != dev or not workspace.is_contiguous():
+                raise VerifyAttnError("the workspace is not a dense tensor of the same device")
             a.workspace = workspace.data_ptr()
             a.workspace_bytes = workspace.numel() * workspace.element_size()
-        _check(lib.va_key_weights(ctypes.byref(a), _stream()), "va_key_weights")
+        _check(lib.va_key_weights(ref, _raw_stream(dev)), "va_key_weights")
     return out
 
 
@@ -515,35 +531,37 @@ def evict_plan(weights, kv_len, budget, *, path=None, accept_len=None, tree_len:
     import torch
     if weights.dim() != 2:
         raise VerifyAttnError("weights are not [B, capacity]")
-    i32, f32 = (torch.int32,), (torch.float32,)
+    dev, i32, f32 = weights.get_device(), torch.int32, torch.float32
     B, cap = weights.shape
     a = VaEvictArgs()
     a.B, a.capacity, a.T, a.n_sink, a.n_recent = B, cap, tree_len, n_sink, n_recent
-    a.weights = _need(weights, "weights", weights, f32, (B, cap))
-    a.kv_len = _need(kv_len, "kv_len", weights, i32, (B,))
-    a.budget = _need(budget, "budget", weights, i32, (B,))
+    a.weights = _need(weights, "weights", dev, f32, (B, cap))
+    a.kv_len = _need(kv_len, "kv_len", dev, i32, (B,))
+    a.budget = _need(budget, "budget", dev, i32, (B,))
     if path is not None:
-        a.path = _need(path, "path", weights, i32, (B, tree_len))
+        a.path = _need(path, "path", dev, i32, (B, tree_len))
     if accept_len is not None:
-        a.accept_len = _need(accept_len, "accept_len", weights, i32, (B,))
+        a.accept_len = _need(accept_len, "accept_len", dev, i32, (B,))
     if pos is not None:
-        a.pos = _need(pos, "pos", weights, i32, (B, cap))
+        a.pos = _need(pos, "pos", dev, i32, (B, cap))
     elif pos_out is not None:
         raise VerifyAttnError("pos_out without pos")
     if req_status is not None:
-        a.req_status = _need(req_status, "req_status", weights, i32, (B,))
+        a.req_status = _need(req_status, "req_status", dev, i32, (B,))
     with _on(weights, stream):
-        new_len, from_slot = torch.empty_like(kv_len), torch.empty(B, cap, device=weights.device,
-                                                                   dtype=torch.int32)
+        new_len = torch.empty_like(kv_len)
+        from_slot = torch.empty_like(weights, dtype=i32)
         a.new_len, a.from_slot = new_len.data_ptr(), from_slot.data_ptr()
         if weights_out is None:
             weights_out = torch.empty_like(weights)
-        a.weights_out = _need(weights_out, "weights_out", weights, f32, (B, cap))
+            a.weights_out = weights_out.data_ptr()
+        else:
+            a.weights_out = _need(weights_out, "weights_out", dev, f32, (B, cap))
         if pos is not None:
             if pos_out is None:
                 pos_out = torch.empty_like(pos)
-            a.pos_out = _need(pos_out, "pos_out", weights, i32, (B, cap))
-        _check(load_library().va_evict_plan(ctypes.byref(a), _stream()), "va_evict_plan")
+            a.pos_out = _need(pos_out, "pos_out", dev, i32, (B, cap))
+        _check(load_library().va_evict_plan(ctypes.byref(a), _raw_stream(dev)), "va_evict_plan")
     return EvictPlan(new_len, from_slot, weights_out, pos_out)
 
 
@@ -554,17 +572,18 @@ def kv_move(c_kv, k_pe, page_table, from_slot, new_len, *, req_status=None, stre
     8-bit codes); from_slot and new_len are the plan's.  Every page up to a request's
     old length must be that request's alone."""
     import torch
-    i32 = (torch.int32,)
+    dev, i32 = c_kv.get_device(), torch.int32
     n, (B, m) = c_kv.shape[0], page_table.shape
-    kinds = (torch.float32, torch.bfloat16, torch.uint8, torch.float8_e4m3fn)
+    if c_kv.dtype is not torch.float32 and c_kv.dtype is not torch.bfloat16 and not _fp8_cache(c_kv):
+        raise VerifyAttnError(f"c_kv is {c_kv.dtype}: not a cache type")
     if B == 0:
         return
-    c = _need(c_kv, "c_kv", c_kv, kinds, (n, PAGE_SIZE, D_LATENT))
-    k = _need(k_pe, "k_pe", c_kv, (c_kv.dtype,), (n, PAGE_SIZE, D_ROPE))
-    t = _need(page_table, "page_table", c_kv, i32, (B, m))
-    f = _need(from_slot, "from_slot", c_kv, i32, (B, m * PAGE_SIZE))
-    l = _need(new_len, "new_len", c_kv, i32, (B,))
-    s = None if req_status is None else _need(req_status, "req_status", c_kv, i32, (B,))
+    c = _need(c_kv, "c_kv", dev, c_kv.dtype, (n, PAGE_SIZE, D_LATENT))
+    k = _need(k_pe, "k_pe", dev, c_kv.dtype, (n, PAGE_SIZE, D_ROPE))
+    t = _need(page_table, "page_table", dev, i32, (B, m))
+    f = _need(from_slot, "from_slot", dev, i32, (B, m * PAGE_SIZE))
+    l = _need(new_len, "new_len", dev, i32, (B,))
+    s = None if req_status is None else _need(req_status, "req_status", dev, i32, (B,))
     with _on(c_kv, stream):
         _check(load_library().va_kv_move(c, k, c_kv.element_size(), n, PAGE_SIZE, t, B, m, f, l, s,
-                                         _stream()), "va_kv_move")
+                                         _raw_stream(dev)), "va_kv_move")

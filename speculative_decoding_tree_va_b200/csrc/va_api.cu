@@ -12,7 +12,7 @@
 namespace {
 
 constexpr int kDefaultSms = 148;  // B200; used when no device can be queried
-constexpr int kMaxDevices = 128;
+using va::kMaxDevices;
 std::atomic<int> g_sm_count[kMaxDevices];  // 0 = not looked up yet
 
 // SM count of the current device (the split planner's wave size), looked up

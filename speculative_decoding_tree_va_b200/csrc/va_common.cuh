@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "../../include/verifyattn.h"
 
 namespace va {
@@ -185,6 +187,22 @@ cudaError_t launch_attn_tc(const va_attn_args& a, SplitRange sp, const int32_t* 
                            float* o_part, float* lse_part, cudaStream_t st, float out_scale);
 cudaError_t launch_kv_widen(const va_attn_args& a, void* w_ckv, void* w_kpe, int32_t* w_table,
                             cudaStream_t st);
+
+// Raises a kernel's dynamic shared memory limit, once per kernel and device (`done`
+// is a static array of the kernel's); always to the same value, so that calls
+// from several host threads cannot undo each other.
+constexpr int kMaxDevices = 128;
+template <typename K>
+cudaError_t raise_smem_once(K* kernel, int bytes, std::atomic<bool> (&done)[kMaxDevices]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const bool known = dev >= 0 && dev < kMaxDevices;
+  if (known && done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && known) done[dev].store(true, std::memory_order_relaxed);
+  return e;
+}
 
 // Around the verify call (va_logprobs.cu, va_evict.cu); `sms` is the device's
 // SM count, which the launch shapes are planned for.

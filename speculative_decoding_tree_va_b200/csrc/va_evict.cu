@@ -632,9 +632,10 @@ cudaError_t launch_evict_plan(const va_evict_args& a, int sms, cudaStream_t st) 
   const bool held = run <= kMaxRun;
   const int bytes = held ? kNT * run * 4 + kNT * run / 8 + 4 : slots / kVec;
   auto* kernel = held ? evict_plan_kernel<true> : evict_plan_kernel<false>;
-  if (bytes > 24 * 1024) {  // past the default limit; the same value from every thread
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         held ? kNT * kMaxRun * 4 + kNT * kMaxRun / 8 + 4 : kMaxKeepBytes);
+  if (bytes > 24 * 1024) {  // past the default limit, beside the static arrays
+    static std::atomic<bool> done[2][kMaxDevices];
+    cudaError_t e = raise_smem_once(
+        kernel, held ? kNT * kMaxRun * 4 + kNT * kMaxRun / 8 + 4 : kMaxKeepBytes, done[held]);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchAttribute at[1];

@@ -812,10 +812,14 @@ cudaError_t launch_kweights_tc(const va_key_weight_args& a, const KwParams& p, i
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  QMaps tq;
+  QMaps tq = {};
   CUtensorMap tckv, tkpe;
   const uint64_t pool = (uint64_t)a.num_pages * kPage;
-  for (int i = 0; i < kBoxes; ++i)
+  // the boxes that halves (multiples of 32 rows) take in these runs: the run's own
+  // power of two, and 32 beside 64
+  int tallest = kBoxes - 1;
+  while (tallest > 0 && tp.run % (8 << tallest)) --tallest;
+  for (int i = tallest == kBoxes - 1 ? tallest - 1 : tallest; i <= tallest; ++i)
     if (!encode_rows(&tq.nope[i], qn, rows, kDc, 8 << i, f8 ? Elem::f16 : Elem::bf16) ||
         !encode_rows(&tq.pe[i], qp, rows, kDr, 8 << i, f8 ? Elem::f16 : Elem::bf16))
       return cudaErrorInvalidValue;
@@ -825,7 +829,8 @@ cudaError_t launch_kweights_tc(const va_key_weight_args& a, const KwParams& p, i
   const long long tiles = (long long)a.B * (((long long)a.max_pages * kPage + kTileKeys - 1) / kTileKeys);
   const int pairs = (int)(tiles < sms / 2 ? tiles : sms / 2);
   auto* k = f8 ? kweights_tc_kernel<true> : kweights_tc_kernel<false>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+  static std::atomic<bool> done[2][kMaxDevices];
+  cudaError_t e = raise_smem_once(k, (int)kSmemBytes, done[f8]);
   if (e != cudaSuccess) return e;
   const int threads = (f8 ? kWarps<true> : kWarps<false>) * 32;
   k<<<2 * pairs, threads, kSmemBytes, st>>>(tq, tckv, tkpe, tp);
