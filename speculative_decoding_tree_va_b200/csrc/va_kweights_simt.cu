@@ -22,6 +22,13 @@ constexpr int kThreads = 256;
 constexpr int kBK = 16;              // dims per step
 constexpr int kPitch = kKwKeys + 4;  // shared row of one dim
 
+// Two buffers of a step; the keys' sums at the end share the space.
+struct Stage {
+  float k[2][kBK][kPitch];
+  float q[2][kBK][kPitch];
+};
+static_assert(sizeof(Stage) >= kThreads / 16 * kKwKeys * sizeof(float), "sums fit");
+
 __device__ __forceinline__ float ex2f(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -58,11 +65,10 @@ __device__ __forceinline__ void load8(const __nv_fp8_e4m3* p, float (&x)[8]) {
 
 template <typename TQ, typename TK>
 __global__ void __launch_bounds__(kThreads, 2) kweights_simt_kernel(const KwParams p) {
-  __shared__ __align__(16) float sK[2][kBK][kPitch];
-  __shared__ __align__(16) float sQ[2][kBK][kPitch];
+  __shared__ __align__(16) Stage st;
   __shared__ float sLse[kKwRows];
   __shared__ uint64_t sMask[kKwRows][2];
-  __shared__ float sSum[kThreads / 16][kKwKeys];
+  float (*sSum)[kKwKeys] = reinterpret_cast<float(*)[kKwKeys]>(&st);
   const int tid = threadIdx.x;
   const int b = blockIdx.y, split = blockIdx.z, j0 = blockIdx.x * kKwKeys;
   const KwRequest rq = kw_request(p, b);
@@ -98,45 +104,63 @@ __global__ void __launch_bounds__(kThreads, 2) kweights_simt_kernel(const KwPara
     const TQ* qp = reinterpret_cast<const TQ*>(p.q_pe) + (size_t)max(g, 0) * kDr;
     if (tid < kKwRows) kw_row_info(p, b, g, node, &sLse[sr], sMask[sr]);
 
-    float fk[8], fq[8];
-    auto fetch = [&](int d0) {
+    float x[8];
+    auto fetch_k = [&](int d0) {
       const int d = d0 + sd;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) fk[i] = fq[i] = 0.f;
+      for (int i = 0; i < 8; ++i) x[i] = 0.f;
       if (krow >= 0) {
-        if (d < kDc) load8(kc + d, fk); else load8(kp + d - kDc, fk);
-      }
-      if (g >= 0) {
-        if (d < kDc) load8(qn + d, fq); else load8(qp + d - kDc, fq);
+        if (d < kDc) load8(kc + d, x); else load8(kp + d - kDc, x);
       }
     };
-    auto put = [&](int buf) {
+    auto fetch_q = [&](int d0) {
+      const int d = d0 + sd;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        sK[buf][sd + i][sr] = fk[i];
-        sQ[buf][sd + i][sr] = fq[i];
+      for (int i = 0; i < 8; ++i) x[i] = 0.f;
+      if (g >= 0) {
+        if (d < kDc) load8(qn + d, x); else load8(qp + d - kDc, x);
       }
     };
+    auto put = [&](float (&to)[kBK][kPitch]) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) to[sd + i][sr] = x[i];
+    };
+    // A step's keys are loaded while its first half is multiplied and its rows while
+    // the second is, so that 8 registers hold them; the operands of a dim are read
+    // from shared memory one dim ahead, because 4 warps a scheduler do not hide it.
     float acc[8][8] = {};  // [row][key]
-    fetch(0);
-    put(0);
+    fetch_k(0);
+    put(st.k[0]);
+    fetch_q(0);
+    put(st.q[0]);
     __syncthreads();
     for (int s = 0; s < kDqk / kBK; ++s) {
-      if (s + 1 < kDqk / kBK) fetch((s + 1) * kBK);
       const int cur = s & 1;
+      const bool more = s + 1 < kDqk / kBK;
+      float k[2][8], q[2][8];
+      auto operands = [&](int d) {
+        float* kd = k[d & 1];
+        float* qd = q[d & 1];
+        *reinterpret_cast<float4*>(kd) = *reinterpret_cast<const float4*>(&st.k[cur][d][tx * 4]);
+        *reinterpret_cast<float4*>(kd + 4) = *reinterpret_cast<const float4*>(&st.k[cur][d][64 + tx * 4]);
+        *reinterpret_cast<float4*>(qd) = *reinterpret_cast<const float4*>(&st.q[cur][d][ty * 4]);
+        *reinterpret_cast<float4*>(qd + 4) = *reinterpret_cast<const float4*>(&st.q[cur][d][64 + ty * 4]);
+      };
+      if (more) fetch_k((s + 1) * kBK);
+      operands(0);
 #pragma unroll
       for (int d = 0; d < kBK; ++d) {
-        float k[8], q[8];
-        *reinterpret_cast<float4*>(&k[0]) = *reinterpret_cast<float4*>(&sK[cur][d][tx * 4]);
-        *reinterpret_cast<float4*>(&k[4]) = *reinterpret_cast<float4*>(&sK[cur][d][64 + tx * 4]);
-        *reinterpret_cast<float4*>(&q[0]) = *reinterpret_cast<float4*>(&sQ[cur][d][ty * 4]);
-        *reinterpret_cast<float4*>(&q[4]) = *reinterpret_cast<float4*>(&sQ[cur][d][64 + ty * 4]);
+        if (d + 1 < kBK) operands(d + 1);
+        if (d == kBK / 2 && more) {
+          put(st.k[cur ^ 1]);
+          fetch_q((s + 1) * kBK);
+        }
 #pragma unroll
         for (int r = 0; r < 8; ++r)
 #pragma unroll
-          for (int c = 0; c < 8; ++c) acc[r][c] = fmaf(q[r], k[c], acc[r][c]);
+          for (int c = 0; c < 8; ++c) acc[r][c] = fmaf(q[d & 1][r], k[d & 1][c], acc[r][c]);
       }
-      if (s + 1 < kDqk / kBK) put(cur ^ 1);
+      if (more) put(st.q[cur ^ 1]);
       __syncthreads();
     }
     const bool tail = j0 + kKwKeys > P;
@@ -194,13 +218,11 @@ cudaError_t launch_kweights_simt(const va_key_weight_args& a, const KwParams& p,
   const dim3 grid((unsigned)((p.max_pages * kPage + kKwKeys - 1) / kKwKeys), (unsigned)p.B,
                   (unsigned)p.splits);
   const bool fp8 = a.flags & VA_FLAG_KV_FP8_E4M3;
-  if (a.dtype == VA_F32) {
-    if (fp8) kweights_simt_kernel<float, __nv_fp8_e4m3><<<grid, kThreads, 0, st>>>(p);
-    else kweights_simt_kernel<float, float><<<grid, kThreads, 0, st>>>(p);
-  } else {
-    if (fp8) kweights_simt_kernel<__nv_bfloat16, __nv_fp8_e4m3><<<grid, kThreads, 0, st>>>(p);
-    else kweights_simt_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, kThreads, 0, st>>>(p);
-  }
+  const bool f32 = a.dtype == VA_F32;
+  auto* k = f32 ? (fp8 ? kweights_simt_kernel<float, __nv_fp8_e4m3> : kweights_simt_kernel<float, float>)
+                : (fp8 ? kweights_simt_kernel<__nv_bfloat16, __nv_fp8_e4m3>
+                       : kweights_simt_kernel<__nv_bfloat16, __nv_bfloat16>);
+  k<<<grid, kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
