@@ -17,10 +17,11 @@
 // all requests, in order and weighted by what they cost, are divided into
 // equal contiguous ranges, one per pair.
 //
-// FP8 cache: the codes come through a ring of their own, and converter warps
-// write them as fp16, which holds every E4M3 value; the queries are multiplied
-// by a power of two per row and stored as fp16 by a first kernel (exact down
-// to 2^-39 of the row's largest element), and the epilogue undoes it in fp32.
+// FP8 cache: the codes are the product's operand as they are (kind::f8f6f4), in
+// chunks of 128 dims; a first kernel multiplies each query row by a power of two
+// and writes it as the sum of three E5M2 numbers.  Three of 3 significant bits
+// hold the 8 of a bf16, down to 2^-31 of the row's largest element, so three
+// products add up to the exact one; the epilogue undoes the power in fp32.
 //
 // Bound by HBM for few rows (1152 or 576 bytes a key) and by the tensor cores
 // for many (128 clocks per 256 x 256 x 16), with the latency of the rings'
@@ -37,19 +38,22 @@ namespace {
 
 using namespace tc;
 
-constexpr int kTileKeys = 256;       // of the pair
-constexpr int kChunks = 9;           // 64-dim chunks of a row: 8 of c_kv, 1 of k_pe
-constexpr int kKChunk = 128 * 128;   // bytes: 128 keys x 64 dims
-constexpr int kMaxK = 12, kMaxQ = 8; // ring slots, at most (codes: kMaxRaw = kMaxK)
-constexpr int kRegion = kChunks * kKChunk + kChunks * 64 * 128;  // keys and rows: 216 KB
-constexpr int kMaxRaw = 12, kRawSlot = 128 * 64;  // FP8 codes: 128 keys x 64 dims
+constexpr int kTileKeys = 256;        // of the pair
+constexpr int kKSlot = 128 * 128;     // bytes of a key chunk: 128 keys x 128 bytes
+constexpr int kMaxK = 12, kMaxQ = 8;  // ring slots, at most
+constexpr int kRegion = 9 * kKSlot + 9 * 64 * 128;  // keys and rows: 216 KB
 constexpr int kWarpK = 0, kWarpMma = 1, kWarpEpi = 2, kWarpQ = 10, kWarpInfo = 11;
-constexpr int kConvWarps = 8, kConvTeams = 4;  // a team converts every 4th chunk
-// Warps of column data: two for a bf16 cache, whose passes may be short; with an
-// FP8 cache one, which leaves 96 registers a thread beside the converters.
-template <bool F8> constexpr int kInfoWarps = F8 ? 1 : 2;
-template <bool F8> constexpr int kWarpConv = kWarpInfo + kInfoWarps<F8>;
-template <bool F8> constexpr int kWarps = kWarpConv<F8> + (F8 ? kConvWarps : 0);
+constexpr int kThreads = 13 * 32;     // two warps of column data
+
+// A row's dims in chunks of 128 bytes: 8 of c_kv and one of k_pe in bf16, 4 of
+// c_kv and half a one of k_pe in FP8; planes: numbers that a query element is the
+// sum of.
+template <bool F8>
+struct Chunks {
+  static constexpr int n = F8 ? 5 : 9, planes = F8 ? 3 : 1;
+  static constexpr int row_bytes = F8 ? 3 * (kDc + kDr) : 2 * (kDc + kDr);  // of a query row
+  static __device__ __forceinline__ int width(int kc) { return F8 && kc == n - 1 ? 64 : 128; }
+};
 
 struct TcParams {
   KwParams k;
@@ -66,7 +70,6 @@ struct QMaps {
 struct __align__(16) Ctl {
   uint64_t k_full[kMaxK], k_empty[kMaxK];
   uint64_t q_full[kMaxQ], q_empty[kMaxQ];
-  uint64_t raw_full[kMaxRaw], raw_empty[kMaxRaw];
   uint64_t r_full;                 // rows that stay
   uint64_t seg_done;               // a request's last tile of this pair is multiplied
   uint64_t s_full[2], s_empty[2];  // scores in tensor memory
@@ -98,15 +101,13 @@ __device__ __forceinline__ float ex2f(float x) {
 }
 
 // How the rows of a request are multiplied: `blocks` passes of `cols` columns.
-// Up to kStay rows stay in shared memory: with more, fewer than 7 key chunks
+// Up to kStay rows stay in shared memory: with more, fewer than 6 key chunks
 // would be in flight beside them, which HBM's latency needs (4 slots beside 256
-// rows took 8000 clocks a tile, rows through the ring 5000).  With an FP8 cache
-// it is the codes that HBM's latency holds up: their ring gets the room, and 4
-// slots do for the key chunks on their way from the converters.
+// rows took 8000 clocks a tile, rows through the ring 5000).
 template <bool F8>
 struct Shape {
-  static constexpr int kStay = F8 ? 192 : 160, kPass = F8 ? 128 : 256;
-  static constexpr int kConvRing = 4 * kKChunk, kRawBeside = 5;
+  using Ch = Chunks<F8>;
+  static constexpr int kStay = F8 ? 128 : 160, kPass = F8 ? 128 : 256;
   int blocks, cols;
   bool stay;
   __device__ __forceinline__ void set(int R) {
@@ -114,26 +115,22 @@ struct Shape {
     blocks = stay ? 1 : (R + kPass - 1) / kPass;
     cols = max(64, ((R + blocks - 1) / blocks + 63) & ~63);
   }
-  // ring slots, and where keys, rows and codes lie in the region
-  __device__ __forceinline__ int rows_stay() const { return kChunks * cols * 64; }
+  // ring slots, and where keys and rows lie in the region
+  __device__ __forceinline__ int rows_stay() const { return cols / 2 * Ch::row_bytes; }
   __device__ __forceinline__ int k_slots() const {
-    return !stay ? kChunks : F8 ? 4 : min(kMaxK, (kRegion - rows_stay()) / kKChunk);
+    return stay ? min(kMaxK, (kRegion - rows_stay()) / kKSlot) : Ch::n;
   }
   __device__ __forceinline__ int k_at() const { return stay ? rows_stay() : 0; }
+  __device__ __forceinline__ int q_slot() const { return cols / 2 * 128 * Ch::planes; }
   __device__ __forceinline__ int q_slots() const {
-    return min(kMaxQ, (kRegion - kChunks * kKChunk - (F8 ? kRawBeside * kRawSlot : 0)) / (cols * 64));
+    return min(kMaxQ, (kRegion - Ch::n * kKSlot) / q_slot());
   }
-  __device__ __forceinline__ int q_at() const { return stay ? 0 : kChunks * kKChunk; }
-  __device__ __forceinline__ int raw_slots() const {
-    return stay ? min(kMaxRaw, (kRegion - rows_stay() - kConvRing) / kRawSlot) : kRawBeside;
-  }
-  __device__ __forceinline__ int raw_at() const {
-    return stay ? rows_stay() + kConvRing : kRegion - kRawBeside * kRawSlot;
-  }
+  __device__ __forceinline__ int q_at() const { return stay ? 0 : Ch::n * kKSlot; }
   // Clocks of a tile, as measured: few rows wait for the keys' share of HBM, rows
   // through the ring for its latency (5400 a pass of 192 columns, 6500 of 256).
   __device__ __forceinline__ int cost() const {
-    return stay ? max(F8 ? 3400 : 5400, 18 * cols + 1000) : blocks * (2200 + 17 * cols) + 300;
+    const int column = F8 ? 27 : 18;
+    return stay ? max(F8 ? 3400 : 5400, column * cols + 1000) : blocks * (2200 + column * cols) + 300;
   }
 };
 
@@ -195,10 +192,10 @@ struct Ring {
 };
 
 template <bool F8>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWarps<F8> * 32, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ CUtensorMap tm_ckv,
                    const __grid_constant__ CUtensorMap tm_kpe, const __grid_constant__ TcParams tp) {
-  constexpr int kThreads = kWarps<F8> * 32;
+  using Ch = Chunks<F8>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   Ctl& c = *reinterpret_cast<Ctl*>(sm + kRegion);
@@ -213,16 +210,12 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
 
   if (tid == 0) {
     for (int i = 0; i < kMaxK; ++i) {
-      mbar_init(&c.k_full[i], F8 ? 2 * (kConvWarps / kConvTeams) : 1);
+      mbar_init(&c.k_full[i], 1);
       mbar_init(&c.k_empty[i], 1);
     }
     for (int i = 0; i < kMaxQ; ++i) {
       mbar_init(&c.q_full[i], 1);
       mbar_init(&c.q_empty[i], 1);
-    }
-    for (int i = 0; i < kMaxRaw; ++i) {
-      mbar_init(&c.raw_full[i], 1);
-      mbar_init(&c.raw_empty[i], kConvWarps / kConvTeams);
     }
     mbar_init(&c.r_full, 1);
     mbar_init(&c.seg_done, 1);
@@ -335,45 +328,38 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
   };
 
   if (warp == kWarpK) {
-    // -------------------------------------------------- key chunks (or codes) by TMA
+    // ------------------------------------------------------------- key chunks by TMA
     bool go = true;
     Ring ring;
     const int oob = p.num_pages * kPage;  // past the pool: zeros
     for (; w.alive() && go; w.next()) {
-      if (new_request(go)) ring.restart(F8 ? w.sh.raw_slots() : w.sh.k_slots());
+      if (new_request(go)) ring.restart(w.sh.k_slots());
       const int key = w.tile * kTileKeys + (int)rank * 128;
       int r0 = kw_pool_row(p, w.b, w.kv_len, key);
       int r1 = kw_pool_row(p, w.b, w.kv_len, key + kPage);
       r0 = r0 < 0 ? oob : r0;
       r1 = r1 < 0 ? oob : r1;
-      uint8_t* ring_at = sm + (F8 ? w.sh.raw_at() : w.sh.k_at());
-      for (int kc = 0; kc < kChunks && go; ++kc) {
+      for (int kc = 0; kc < Ch::n && go; ++kc) {
         const int s = ring.slot;
-        go = wait(F8 ? &c.raw_empty[s] : &c.k_empty[s], ring.phase() ^ 1);
+        go = wait(&c.k_empty[s], ring.phase() ^ 1);
         if (!go) break;
         if (elect_one()) {
-          const CUtensorMap* map = kc < 8 ? &tm_ckv : &tm_kpe;
-          const int x = kc < 8 ? kc * 64 : 0;
-          if (F8) {
-            arrive_expect_tx(&c.raw_full[s], kRawSlot);
-            const uint32_t dst = smem_u32(ring_at + s * kRawSlot);
-            tma_2d_local(dst, map, &c.raw_full[s], x, r0);
-            tma_2d_local(dst + kRawSlot / 2, map, &c.raw_full[s], x, r1);
-          } else {
-            const uint32_t bar = map_to_rank(smem_u32(&c.k_full[s]), 0);
-            if (rank == 0) arrive_expect_tx(&c.k_full[s], 2 * kKChunk);
-            const uint32_t dst = smem_u32(ring_at + s * kKChunk);
-            tma_2d(dst, map, bar, x, r0);
-            tma_2d(dst + kKChunk / 2, map, bar, x, r1);
-          }
+          const bool pe = kc == Ch::n - 1;
+          const CUtensorMap* map = pe ? &tm_kpe : &tm_ckv;
+          const int x = pe ? 0 : kc * (F8 ? 128 : 64);
+          const int bytes = 128 * Ch::width(kc);
+          const uint32_t bar = map_to_rank(smem_u32(&c.k_full[s]), 0);
+          if (rank == 0) arrive_expect_tx(&c.k_full[s], 2 * bytes);
+          const uint32_t dst = smem_u32(sm + w.sh.k_at() + s * kKSlot);
+          tma_2d(dst, map, bar, x, r0);
+          tma_2d(dst + bytes / 2, map, bar, x, r1);
         }
         __syncwarp();
         ring.advance();
       }
     }
     // the last use of every slot must be over before the CTA may exit
-    for (int s = 0; s < kMaxK && go; ++s)
-      go = wait(F8 ? &c.raw_empty[s] : &c.k_empty[s], ((ring.used >> s) & 1u) ^ 1);
+    for (int s = 0; s < kMaxK && go; ++s) go = wait(&c.k_empty[s], ((ring.used >> s) & 1u) ^ 1);
     if (go) wait(&c.seg_done, seg_parity);
     if (*abort) settle();
   } else if (warp == kWarpQ) {
@@ -394,35 +380,40 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
       const bool fresh = new_request(go);
       if (!go || (!fresh && w.sh.stay)) continue;
       if (fresh) ring.restart(!w.sh.stay ? w.sh.q_slots() : 1);
-      const int half = w.sh.cols / 2, bytes = half * 128;
+      const int half = w.sh.cols / 2;
       int box = kBoxes - 1;  // the tallest box that fits the half and the run
       while (box > 0 && ((half | tp.run) & ((8 << box) - 1))) --box;
       const int box_rows = 8 << box;
-      const CUtensorMap* tm_qn = &tm_q.nope[box];
-      const CUtensorMap* tm_qp = &tm_q.pe[box];
       const bool mine = lane < half / box_rows;
-      uint8_t* at = sm + w.sh.q_at() + lane * box_rows * 128;
       for (int rb = 0; rb < w.sh.blocks && go; ++rb) {
         const int y = mine ? map_row(rb * w.sh.cols + (int)rank * half + lane * box_rows) : 0;
-        if (w.sh.stay) {  // all nine chunks at once, to stay
-          if (lane == 0 && rank == 0) arrive_expect_tx(&c.r_full, 2 * bytes * kChunks);
+        // this lane's boxes of a chunk, one a plane
+        auto boxes = [&](int kc, uint8_t* at, uint32_t bar) {
+          const bool pe = kc == Ch::n - 1;
+          const int wide = Ch::width(kc), e = F8 ? 1 : 2;
+          for (int pl = 0; pl < Ch::planes; ++pl)
+            tma_2d(smem_u32(at + (pl * half + lane * box_rows) * wide),
+                   pe ? &tm_q.pe[box] : &tm_q.nope[box], bar,
+                   pl * (pe ? kDr : kDc) + (pe ? 0 : kc * (128 / e)), y);
+        };
+        if (w.sh.stay) {  // all chunks at once
+          if (lane == 0 && rank == 0) arrive_expect_tx(&c.r_full, 2 * w.sh.rows_stay());
           __syncwarp();
           const uint32_t bar = map_to_rank(smem_u32(&c.r_full), 0);
           if (mine)
-            for (int kc = 0; kc < kChunks; ++kc)
-              tma_2d(smem_u32(at + kc * bytes), kc < 8 ? tm_qn : tm_qp, bar, kc < 8 ? kc * 64 : 0, y);
+            for (int kc = 0; kc < Ch::n; ++kc) boxes(kc, sm + w.sh.q_at() + kc * w.sh.q_slot(), bar);
           __syncwarp();
           continue;
         }
-        for (int kc = 0; kc < kChunks && go; ++kc) {
+        for (int kc = 0; kc < Ch::n && go; ++kc) {
           const int s = ring.slot;
           go = wait(&c.q_empty[s], ring.phase() ^ 1);
           if (!go) break;
-          if (lane == 0 && rank == 0) arrive_expect_tx(&c.q_full[s], 2 * bytes);
+          if (lane == 0 && rank == 0)
+            arrive_expect_tx(&c.q_full[s], w.sh.cols * Ch::planes * Ch::width(kc));
           __syncwarp();
           if (mine)
-            tma_2d(smem_u32(at + s * bytes), kc < 8 ? tm_qn : tm_qp,
-                   map_to_rank(smem_u32(&c.q_full[s]), 0), kc < 8 ? kc * 64 : 0, y);
+            boxes(kc, sm + w.sh.q_at() + s * w.sh.q_slot(), map_to_rank(smem_u32(&c.q_full[s]), 0));
           __syncwarp();
           ring.advance();
         }
@@ -437,10 +428,8 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
       bool ok = true;
       Ring kring, qring;
       uint32_t rphase = 0, pass = 0;
-      const uint64_t desc = sw128_desc(smem_u32(sm));
       for (; w.alive() && ok; w.next()) {
         const bool stream = !w.sh.stay;
-        const int bytes = w.sh.cols * 64;  // of a chunk of this CTA's rows
         if (held != w.b) {
           held = w.b;
           kring.restart(w.sh.k_slots());
@@ -450,11 +439,12 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
             rphase ^= 1;
           }
         }
-        // kind::f16: fp32 sums; A, B bf16 (1) or fp16 (0), K-major; M = 256
-        const uint32_t idesc = (1u << 4) | (F8 ? 0u : (1u << 7) | (1u << 10)) |
+        // fp32 sums; K-major A and B: bf16 (1, 1) of kind::f16, or E4M3 (0) and E5M2 (1)
+        // of kind::f8f6f4; M = 256
+        const uint32_t idesc = (1u << 4) | (F8 ? 0u : 1u << 7) | (1u << 10) |
                                ((uint32_t)(w.sh.cols >> 3) << 17) | ((uint32_t)(256 >> 4) << 24);
-        const uint64_t dk = desc + (uint64_t)(w.sh.k_at() >> 4);
-        const uint64_t dq = desc + (uint64_t)(w.sh.q_at() >> 4);
+        const uint32_t k0 = smem_u32(sm + w.sh.k_at()), q0 = smem_u32(sm + w.sh.q_at());
+        const int q_slot = w.sh.q_slot(), half = w.sh.cols / 2;
         const bool seg_end = w.last_of_request();
         const Ring first = kring;  // the tile's first chunk: every block begins there
         for (int rb = 0; rb < w.sh.blocks && ok; ++rb, ++pass) {
@@ -462,22 +452,38 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
           const bool last = rb == w.sh.blocks - 1;
           if (rb > 0) kring = first;
           ok = wait(&c.s_empty[pass & 1], ((pass >> 1) & 1) ^ 1);
-          for (int kc = 0; kc < kChunks && ok; ++kc) {
+          for (int kc = 0; kc < Ch::n && ok; ++kc) {
             const int ks = kring.slot, qs = qring.slot;
             if (rb == 0) ok = wait(&c.k_full[ks], kring.phase());
             if (ok && stream) ok = wait(&c.q_full[qs], qring.phase());
             if (!ok) break;
             if (elect_one()) {
               fence_after();
-              const uint64_t a = dk + (uint64_t)((ks * kKChunk) >> 4);
-              const uint64_t b = dq + (uint64_t)(((stream ? qs : kc) * bytes) >> 4);
-              mma_pair(d, a, b, idesc, kc != 0);
-              mma_pair(d, a + 2, b + 2, idesc, 1u);
-              mma_pair(d, a + 4, b + 4, idesc, 1u);
-              mma_pair(d, a + 6, b + 6, idesc, 1u);
+              const uint32_t ka = k0 + ks * kKSlot, qa = q0 + (stream ? qs : kc) * q_slot;
+              if (!F8) {
+                const uint64_t a = sw128_desc(ka), b = sw128_desc(qa);
+                mma_pair(d, a, b, idesc, kc != 0);
+                mma_pair(d, a + 2, b + 2, idesc, 1u);
+                mma_pair(d, a + 4, b + 4, idesc, 1u);
+                mma_pair(d, a + 6, b + 6, idesc, 1u);
+              } else {
+                const bool pe = kc == Ch::n - 1;
+                const uint64_t a = pe ? sw64_desc(ka) : sw128_desc(ka);
+#pragma unroll 1
+                for (int pl = 0; pl < Ch::planes; ++pl) {
+                  const uint32_t at = qa + pl * half * (pe ? 64 : 128);
+                  const uint64_t b = pe ? sw64_desc(at) : sw128_desc(at);
+                  mma_pair_f8(d, a, b, idesc, kc + pl != 0);
+                  mma_pair_f8(d, a + 2, b + 2, idesc, 1u);
+                  if (!pe) {
+                    mma_pair_f8(d, a + 4, b + 4, idesc, 1u);
+                    mma_pair_f8(d, a + 6, b + 6, idesc, 1u);
+                  }
+                }
+              }
               if (stream) commit_pair(&c.q_empty[qs]);
               if (last) commit_pair(&c.k_empty[ks]);
-              if (kc == kChunks - 1) {
+              if (kc == Ch::n - 1) {
                 commit_pair(&c.s_full[pass & 1]);
                 if (last && seg_end) commit_pair(&c.seg_done);
               }
@@ -494,66 +500,7 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
         final_wait(&c.drain, 0);
       }
     }
-  } else if (F8 && warp >= kWarpConv<F8>) {
-    // ------------------------------------------------------- FP8 codes to fp16 chunks
-    // The teams work on different chunks at once, because a chunk's path (code wait,
-    // loads, conversion, stores, proxy fence, arrival) takes over 1000 clocks.  Two
-    // warps a team, 64 keys each: lane l has codes 16 (l & 3) .. of keys l / 4 + 8 i.
-    // A phase bit cannot tell a slot's last use from the one two before, so a team
-    // must not ask for a slot whose last use another team is still at: with 4 slots
-    // that was its own, and with 9 it is 9 chunks back, while codes arrive only when
-    // the chunks kRawBeside = 5 and more before them are converted.
-    constexpr int kKeysPerWarp = 128 * kConvTeams / kConvWarps;
-    const int cw = warp - kWarpConv<F8>, team = cw % kConvTeams;
-    const int m0 = cw / kConvTeams * kKeysPerWarp, sub = lane >> 2, u0 = lane & 3;
-    const uint32_t full0 = map_to_rank(smem_u32(&c.k_full[0]), 0);
-    bool go = true;
-    Ring raw, ring;
-    int turn = 0;
-    for (; w.alive() && go; w.next()) {
-      if (new_request(go)) {
-        ring.restart(w.sh.k_slots());
-        raw.restart(w.sh.raw_slots());
-      }
-      const uint8_t* codes = sm + w.sh.raw_at() + (m0 + sub) * 64 + u0 * 16;
-      uint8_t* k_at = sm + w.sh.k_at() + (m0 + sub) * 128;
-      for (int kc = 0; kc < kChunks && go; ++kc) {
-        if (turn == team) {
-          go = wait(&c.raw_full[raw.slot], raw.phase());
-          if (go) go = wait(&c.k_empty[ring.slot], ring.phase() ^ 1);
-          if (!go) break;
-#pragma unroll 2
-          for (int i = 0; i < kKeysPerWarp / 8; ++i) {
-            const uint4 v = *reinterpret_cast<const uint4*>(codes + raw.slot * kRawSlot + i * 512);
-            const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-            uint32_t o[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const __half2_raw f = __nv_cvt_fp8x2_to_halfraw2(
-                  (__nv_fp8x2_storage_t)(x[j >> 1] >> (16 * (j & 1))), __NV_E4M3);
-              o[j] = (uint32_t)f.x | (uint32_t)f.y << 16;
-            }
-            uint8_t* to = k_at + ring.slot * kKChunk + i * 1024;  // key m0 + sub + 8 i
-            *reinterpret_cast<uint4*>(to + (((2 * u0) ^ sub) << 4)) =
-                make_uint4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<uint4*>(to + (((2 * u0 + 1) ^ sub) << 4)) =
-                make_uint4(o[4], o[5], o[6], o[7]);
-          }
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) {
-            arrive(&c.raw_empty[raw.slot]);
-            arrive_cluster(full0 + ring.slot * 8);
-          }
-        }
-        turn = turn + 1 == kConvTeams ? 0 : turn + 1;
-        raw.advance();
-        ring.advance();
-      }
-    }
-    for (int s = 0; s < kMaxK && go; ++s) go = wait(&c.k_empty[s], ((ring.used >> s) & 1u) ^ 1);
-    if (go) wait(&c.seg_done, seg_parity);
-  } else if (warp >= kWarpInfo && warp < kWarpConv<F8>) {
+  } else if (warp >= kWarpInfo) {
     // ------------------------------------------------------- column data of each pass
     // Ahead of the epilogue, so that their loads are off its path; two warps take
     // turns.
@@ -563,7 +510,7 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
     for (; w.alive() && go; w.next()) {
       for (int rb = 0; rb < w.sh.blocks && go; ++rb, ++pass) {
         const int buf = pass & 1;
-        if (kInfoWarps<F8> == 2 && buf != warp - kWarpInfo) continue;
+        if (buf != warp - kWarpInfo) continue;
         bool free = false;
 #pragma unroll 1
         for (int k0 = 0; k0 * 32 < w.sh.cols && go; k0 += 4) {
@@ -711,9 +658,11 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
   }
 }
 
-// Counted rows of every request, dense from b * T * H on; for an FP8 cache as
-// fp16, multiplied by the power of two that brings the row's largest element
-// to [2^14, 2^15), and its inverse.  One warp per row.
+// Counted rows of every request, dense from b * T * H on.  For an FP8 cache each
+// row is multiplied by the power of two that brings its largest element to [2^14,
+// 2^15), and an element x is written as the E5M2 numbers nearest to x, to what is
+// left of it, and to what is left then: planes [3][512] and [3][64] of a row;
+// `scale` gets the inverse power.  One warp per row.
 template <bool F8>
 __global__ void __launch_bounds__(256)
 kweights_rows_kernel(const KwParams p, uint4* __restrict__ qn, uint4* __restrict__ qp,
@@ -728,40 +677,56 @@ kweights_rows_kernel(const KwParams p, uint4* __restrict__ qn, uint4* __restrict
   const size_t to = (size_t)b * p.T * p.H + r;
   const uint4* sn = reinterpret_cast<const uint4*>(p.q_nope) + (size_t)g * (kDc / 8);
   const uint4* sp = reinterpret_cast<const uint4*>(p.q_pe) + (size_t)g * (kDr / 8);
-  uint4 v[3];
+  uint4 v[3];  // 8 elements each: of q_nope from 8 lane and 256 + 8 lane on, of q_pe from 8 lane
   v[0] = sn[lane];
   v[1] = sn[lane + 32];
   v[2] = lane < 8 ? sp[lane] : make_uint4(0, 0, 0, 0);
-  if (F8) {
-    float big = 0.f;
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        big = fmaxf(big, fmaxf(fabsf(__uint_as_float(u[k] << 16)), fabsf(__uint_as_float(u[k] & 0xffff0000u))));
-    }
-    big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
-    // exponent of 2 to multiply by; zero and non-finite rows stay as they are
-    int ex = 0;
-    if (big > 0.f && big < INFINITY) ex = min(14 - ilogbf(big), 120);
-    const float up = ldexpf(1.f, ex);
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const __half2 h = __floats2half2_rn(__uint_as_float(u[k] << 16) * up,
-                                            __uint_as_float(u[k] & 0xffff0000u) * up);
-        u[k] = *reinterpret_cast<const uint32_t*>(&h);
-      }
-      v[i] = make_uint4(u[0], u[1], u[2], u[3]);
-    }
-    if (lane == 0) scale[to] = ldexpf(1.f, -ex);
+  if (!F8) {
+    qn[to * (kDc / 8) + lane] = v[0];
+    qn[to * (kDc / 8) + lane + 32] = v[1];
+    if (lane < 8) qp[to * (kDr / 8) + lane] = v[2];
+    return;
   }
-  qn[to * (kDc / 8) + lane] = v[0];
-  qn[to * (kDc / 8) + lane + 32] = v[1];
-  if (lane < 8) qp[to * (kDr / 8) + lane] = v[2];
+  float big = 0.f;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      big = fmaxf(big, fmaxf(fabsf(__uint_as_float(u[k] << 16)), fabsf(__uint_as_float(u[k] & 0xffff0000u))));
+  }
+  big = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(big)));
+  // exponent of 2 to multiply by; zero and non-finite rows stay as they are
+  int ex = 0;
+  if (big > 0.f && big < INFINITY) ex = min(14 - ilogbf(big), 120);
+  const float up = ldexpf(1.f, ex);
+  uint2* n8 = reinterpret_cast<uint2*>(qn) + to * (3 * kDc / 8);
+  uint2* p8 = reinterpret_cast<uint2*>(qp) + to * (3 * kDr / 8);
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    if (i == 2 && lane >= 8) break;
+    const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+    uint64_t plane[3] = {0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float x = __uint_as_float(k & 1 ? u[k >> 1] & 0xffff0000u : u[k >> 1] << 16) * up;
+      const bool finite = fabsf(x) < INFINITY;
+#pragma unroll
+      for (int pl = 0; pl < 3; ++pl) {
+        __nv_fp8_storage_t q = __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E5M2);
+        x -= __half2float(__half(__nv_cvt_fp8_to_halfraw(q, __NV_E5M2)));
+        if (!finite) q = pl == 0 ? 0x7f : 0;  // NaN: the row's scores come out as NaN
+        plane[pl] |= (uint64_t)q << (8 * k);
+      }
+    }
+#pragma unroll
+    for (int pl = 0; pl < 3; ++pl) {
+      const uint2 o = make_uint2((uint32_t)plane[pl], (uint32_t)(plane[pl] >> 32));
+      if (i < 2) n8[pl * (kDc / 8) + i * 32 + lane] = o;
+      else p8[pl * (kDr / 8) + lane] = o;
+    }
+  }
+  if (lane == 0) scale[to] = ldexpf(1.f, -ex);
 }
 
 struct RowsLayout {
@@ -771,8 +736,9 @@ RowsLayout rows_layout(const va_key_weight_args& a, bool f8) {
   const size_t rows = (size_t)a.B * a.T * a.H;
   RowsLayout l;
   l.qn = 0;
-  l.qp = align256(rows * kDc * 2);
-  l.scale = l.qp + align256(rows * kDr * 2);
+  const int bytes = f8 ? 3 : 2;
+  l.qp = align256(rows * kDc * bytes);
+  l.scale = l.qp + align256(rows * kDr * bytes);
   l.total = l.scale + (f8 ? align256(rows * sizeof(float)) : 0);
   return l;
 }
@@ -820,11 +786,11 @@ cudaError_t launch_kweights_tc(const va_key_weight_args& a, const KwParams& p, i
   int tallest = kBoxes - 1;
   while (tallest > 0 && tp.run % (8 << tallest)) --tallest;
   for (int i = tallest == kBoxes - 1 ? tallest - 1 : tallest; i <= tallest; ++i)
-    if (!encode_rows(&tq.nope[i], qn, rows, kDc, 8 << i, f8 ? Elem::f16 : Elem::bf16) ||
-        !encode_rows(&tq.pe[i], qp, rows, kDr, 8 << i, f8 ? Elem::f16 : Elem::bf16))
+    if (!encode_rows(&tq.nope[i], qn, rows, kDc * (f8 ? 3 : 2), 8 << i, 128, f8) ||
+        !encode_rows(&tq.pe[i], qp, rows, kDr * (f8 ? 3 : 2), 8 << i, f8 ? 64 : 128, f8))
       return cudaErrorInvalidValue;
-  if (!encode_rows(&tckv, a.c_kv, pool, kDc, kPage, f8 ? Elem::u8 : Elem::bf16) ||
-      !encode_rows(&tkpe, a.k_pe, pool, kDr, kPage, f8 ? Elem::u8 : Elem::bf16))
+  if (!encode_rows(&tckv, a.c_kv, pool, kDc * (f8 ? 1 : 2), kPage, 128, f8) ||
+      !encode_rows(&tkpe, a.k_pe, pool, kDr * (f8 ? 1 : 2), kPage, f8 ? 64 : 128, f8))
     return cudaErrorInvalidValue;
   const long long tiles = (long long)a.B * (((long long)a.max_pages * kPage + kTileKeys - 1) / kTileKeys);
   const int pairs = (int)(tiles < sms / 2 ? tiles : sms / 2);
@@ -832,8 +798,7 @@ cudaError_t launch_kweights_tc(const va_key_weight_args& a, const KwParams& p, i
   static std::atomic<bool> done[2][kMaxDevices];
   cudaError_t e = raise_smem_once(k, (int)kSmemBytes, done[f8]);
   if (e != cudaSuccess) return e;
-  const int threads = (f8 ? kWarps<true> : kWarps<false>) * 32;
-  k<<<2 * pairs, threads, kSmemBytes, st>>>(tq, tckv, tkpe, tp);
+  k<<<2 * pairs, kThreads, kSmemBytes, st>>>(tq, tckv, tkpe, tp);
   return cudaGetLastError();
 }
 

@@ -113,15 +113,6 @@ __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, uin
       ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_leader), "r"(x), "r"(y)
       : "memory");
 }
-// The same, bytes counted on a barrier of this CTA.
-__device__ __forceinline__ void tma_2d_local(uint32_t dst, const CUtensorMap* map, uint64_t* bar,
-                                             int x, int y) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4}], [%2];"
-      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y)
-      : "memory");
-}
 __device__ __forceinline__ void arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -140,6 +131,14 @@ __device__ __forceinline__ void mma_pair(uint32_t d, uint64_t a, uint64_t b, uin
   asm volatile(
       "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
       "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}"
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+}
+// The same for 8-bit floating point operands (their formats are in idesc).
+__device__ __forceinline__ void mma_pair_f8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n.reg .pred p;\nsetp.ne.b32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}"
       ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
 }
 // One arrival on this barrier in both CTAs once the MMAs issued so far are done.
@@ -163,18 +162,21 @@ __device__ __forceinline__ void ld32(uint32_t taddr, float (&v)[32]) {
 __device__ __forceinline__ void wait_ld() {
   asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
-// Shared-memory descriptor of a K-major operand in 128-byte-swizzled rows of
-// 64 16-bit elements (8-row groups 1024 bytes apart).
+// Shared-memory descriptors of K-major operands: rows of 128 bytes, swizzled by
+// 128 (8-row groups 1024 bytes apart), or of 64 swizzled by 64 (512 apart).
 __device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
   return (uint64_t)((saddr >> 4) & 0x3FFF) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 |
          (uint64_t)1 << 46 | (uint64_t)2 << 61;
 }
+__device__ __forceinline__ uint64_t sw64_desc(uint32_t saddr) {
+  return (uint64_t)((saddr >> 4) & 0x3FFF) | (uint64_t)1 << 16 | (uint64_t)(512 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)4 << 61;
+}
 
-// Row-major [rows, cols], boxes of [box_rows x 64 columns]: 16-bit elements in
-// 128-byte-swizzled rows, or bytes in plain rows.
-enum class Elem { bf16, f16, u8 };
-inline bool encode_rows(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t cols,
-                        uint32_t box_rows, Elem elem) {
+// Row-major [rows, row_bytes] of bf16 or bytes, in boxes of [box_rows x box_bytes],
+// box_bytes = 128 or 64, swizzled by as much.
+inline bool encode_rows(CUtensorMap* map, const void* ptr, uint64_t rows, uint64_t row_bytes,
+                        uint32_t box_rows, uint32_t box_bytes, bool bytes) {
   static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() {
     void* p = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -184,16 +186,14 @@ inline bool encode_rows(CUtensorMap* map, const void* ptr, uint64_t rows, uint64
     return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
   }();
   if (!fn) return false;
-  cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {cols * (elem == Elem::u8 ? 1 : 2)};
-  cuuint32_t box[2] = {64, box_rows};
+  const int e = bytes ? 1 : 2;
+  cuuint64_t dims[2] = {row_bytes / e, rows};
+  cuuint64_t strides[1] = {row_bytes};
+  cuuint32_t box[2] = {box_bytes / e, box_rows};
   cuuint32_t estr[2] = {1, 1};
-  const CUtensorMapDataType type = elem == Elem::u8    ? CU_TENSOR_MAP_DATA_TYPE_UINT8
-                                   : elem == Elem::f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                                       : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  return fn(map, type, 2, const_cast<void*>(ptr), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE,
-            elem == Elem::u8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+  return fn(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+            const_cast<void*>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
