@@ -79,14 +79,14 @@ struct __align__(16) Ctl {
   int start_b, start_tile;
   uint32_t tmem;
   int abort;
-  // of each column of a pass: its node, its row's log2-sum and factor; one bit
+  // of each column of a pass: its node, its row's log-sum-exp and factor; one bit
   // where the column adds nothing (no row, absent node, empty row); and the
   // node of all that a group of 32 columns adds (-1: several)
   uint32_t none[2][8];
   int one[2][8];
   float xsum[2][128];
   uint8_t node[2][256];
-  __align__(16) float l2[2][256];
+  __align__(16) float lse[2][256];
   __align__(16) float factor[2][256];  // FP8 cache
 };
 constexpr int kScanAt = offsetof(Ctl, xsum);  // the start-up scan uses xsum ..
@@ -539,8 +539,8 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
             const bool adds = ok[k] && ((word[k] >> (node[k] & 63)) & 1ull) && l[k] != -INFINITY;
             const int e = (k0 + k) * 32 + lane;
             c.node[buf][e] = (uint8_t)node[k];
-            c.l2[buf][e] = l[k] * kLog2e;
-            if (F8) c.factor[buf][e] = adds ? f[k] * (p.scale * kLog2e) : 0.f;
+            c.lse[buf][e] = l[k];
+            if (F8) c.factor[buf][e] = adds ? f[k] * p.scale : 0.f;
             const uint32_t on = __ballot_sync(0xffffffffu, adds);
             const int first = __shfl_sync(0xffffffffu, node[k], on ? __ffs(on) - 1 : 0);
             const bool same = __all_sync(0xffffffffu, !adds || node[k] == first);
@@ -561,7 +561,7 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
     const int q = warp & 3, half = (warp - kWarpEpi) >> 2, m = 32 * q + lane;
     const uint32_t lane_base = (uint32_t)(32 * q) << 16;
     const uint32_t free0 = map_to_rank(smem_u32(&c.s_empty[0]), 0);
-    const float factor = p.scale * kLog2e;
+    const float factor = p.scale;
     const int W = (p.T + 63) >> 6;
     uint32_t pass = 0, tile_no = 0;
     for (; w.alive(); w.next(), ++tile_no) {
@@ -619,18 +619,22 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
               for (int i = 0; i < 32; ++i) off |= (sees(c.node[buf][at + i]) ^ 1u) << i;
             }
           }
-          const float* l2 = &c.l2[buf][at];
+          const float* ls = &c.lse[buf][at];
           const float* fc = &c.factor[buf][at];
+          // scale s - lse first: small where the weight is large, and so its rounding
+          auto prob = [&](float s, int i) {
+            return ex2f(fmaf(s, F8 ? fc[i] : factor, -ls[i]) * kLog2e);
+          };
           if (__any_sync(0xffffffffu, off != 0)) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              const float v = ex2f(fmaf(x[i], F8 ? fc[i] : factor, -l2[i]));
+              const float v = prob(x[i], i);
               sum[i & 3] += (off >> i) & 1u ? 0.f : v;
             }
           } else {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              sum[i & 3] += ex2f(fmaf(x[i], F8 ? fc[i] : factor, -l2[i]));
+              sum[i & 3] += prob(x[i], i);
           }
         }
         __syncwarp();
