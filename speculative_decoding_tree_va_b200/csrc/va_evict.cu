@@ -32,7 +32,7 @@ constexpr int kNT = 1024;
 constexpr int kVec = 4;               // consecutive slots of a thread in a tile
 constexpr int kTile = kNT * kVec;
 constexpr int kBins = 2048;
-constexpr int kBatch = 8;             // loads of a thread in flight
+constexpr int kBatch = 8, kFew = 4;   // loads of a thread in flight
 constexpr int kMaxKeepBytes = 128 * 1024;  // keep bits of a CTA's slots in shared memory
 constexpr int kMaxRun = 32;                // slots of a thread whose keys are held
 constexpr uint32_t kDropped = 0u, kProtected = ~0u;
@@ -97,6 +97,7 @@ __device__ __forceinline__ uint32_t order_bits(float x) {
 
 struct Shared {
   __align__(8) uint32_t hist[2][kBins];
+  __align__(8) uint32_t sum[kBins];  // this CTA's share of the bins, over the cluster
   uint32_t warp_sum[32];
   uint32_t total;
   int32_t newest;                 // of this CTA
@@ -135,6 +136,7 @@ __device__ uint32_t block_scan(uint32_t v, Shared& s, uint32_t* total) {
 
 template <bool Held>
 __global__ void __launch_bounds__(kNT) evict_plan_kernel(const PlanParams p, int C) {
+  static_assert(sizeof(Shared) <= 28 * 1024, "beside 20 KB of dynamic shared memory");
   __shared__ Shared s;
   extern __shared__ uint32_t dyn[];  // keys of this CTA's slots (Held) and their keep bits
   const int tid = threadIdx.x, lane = tid & 31;
@@ -302,24 +304,29 @@ __global__ void __launch_bounds__(kNT) evict_plan_kernel(const PlanParams p, int
         }
         sync();
       }
-      // thread t holds the two highest remaining bins in descending order
+      // The bins over the cluster: of more than two, each CTA adds up its share of
+      // them, so that a bin is read C times and not C * C.  Thread t then holds bins d0 and d0 - 1, the
+      // highest left in descending order.
       uint32_t c0 = 0, c1 = 0;
       const int d0 = bins - 1 - 2 * tid;
-      if (d0 > 0) {
-        if (C > 1) {
-          uint2 v[kMaxCluster];
-#pragma unroll
-          for (int r = 0; r < kMaxCluster; ++r)
-            v[r] = r < C ? remote_u32x2(&h[d0 - 1], r) : make_uint2(0, 0);
-#pragma unroll
-          for (int r = 0; r < kMaxCluster; ++r) {
-            c0 += v[r].y;
-            c1 += v[r].x;
-          }
-        } else {
-          c0 = h[d0];
-          c1 = h[d0 - 1];
+      if (C == 2) {
+        if (d0 > 0) {
+          const uint2 v = remote_u32x2(&h[d0 - 1], 0), u = remote_u32x2(&h[d0 - 1], 1);
+          c0 = v.y + u.y;
+          c1 = v.x + u.x;
         }
+      } else if (C > 1) {
+        const int share = bins / C;
+        for (int i = tid; i < share; i += kNT) s.sum[i] = remote_sum(&h[(int)rank * share + i], C);
+        sync();
+        if (d0 > 0) {
+          const uint2 v = remote_u32x2(&s.sum[(d0 - 1) % share], (uint32_t)((d0 - 1) / share));
+          c0 = v.y;
+          c1 = v.x;
+        }
+      } else if (d0 > 0) {
+        c0 = h[d0];
+        c1 = h[d0 - 1];
       }
       uint32_t total;
       const uint32_t before = block_scan(c0 + c1, s, &total);
@@ -367,33 +374,39 @@ __global__ void __launch_bounds__(kNT) evict_plan_kernel(const PlanParams p, int
     // Indices of its holes and movers: the CTA's (at most 32768 each) in one scan,
     // then the cluster's.  The outputs may overwrite the inputs from here on.
     const uint32_t both = block_scan(__popc(hole) | __popc(mover) << 16, s, &total);
-    if (tid == 0) { s.cnt[2] = total & 0xffffu; s.cnt[3] = total >> 16; }
+    const int holes = (int)(total & 0xffffu), movers = (int)(total >> 16);
+    if (tid == 0) { s.cnt[2] = holes; s.cnt[3] = movers; }
     for (int i = tid; i < (kNT * run + 31) / 32; i += kNT) kept[i] = 0;
+    // their slots in order, in the keys' place: the copies below are then contiguous
+    // on at least one side, where a run's own would touch a sector per slot
+    int* hole_slot = reinterpret_cast<int*>(held);
+    int* mover_slot = hole_slot + holes;
+    for (uint32_t i = both & 0xffffu; hole; hole &= hole - 1) hole_slot[i++] = j0 + __ffs(hole) - 1;
+    for (uint32_t i = both >> 16; mover; mover &= mover - 1) mover_slot[i++] = j0 + __ffs(mover) - 1;
     sync();
     {  // the run's bits, in one or two words
       const int bit = tid * run, sh = bit & 31;
       if (keep) atomicOr(&kept[bit >> 5], keep << sh);
       if (sh && keep >> (32 - sh)) atomicOr(&kept[(bit >> 5) + 1], keep >> (32 - sh));
     }
-    uint32_t hole_at = (both & 0xffffu) + remote_sum(&s.cnt[2], (int)rank);
-    uint32_t mover_at = (both >> 16) + remote_sum(&s.cnt[3], (int)rank);
+    const int hole_at = (int)remote_sum(&s.cnt[2], (int)rank);
+    const int mover_at = (int)remote_sum(&s.cnt[3], (int)rank);
     // list the holes in from_slot[n_new ..): there are as many as movers, which
     // all lie there, so the list fits
-    for (; hole; hole &= hole - 1)
-      p.from_slot[row + n_new + hole_at++] = j0 + __ffs(hole) - 1;
+    int* list = p.from_slot + row + n_new;
+    for (int i = tid; i < holes; i += kNT) list[hole_at + i] = hole_slot[i];
     __threadfence();
     sync();
     // a mover's key goes to its hole, the other kept slots keep theirs
-    while (mover) {
-      constexpr int kFew = 4;
+    for (int i0 = tid; i0 < movers; i0 += kNT * kFew) {
       int j[kFew], to[kFew], q[kFew];
       float x[kFew];
 #pragma unroll
       for (int u = 0; u < kFew; ++u) {
-        j[u] = mover ? j0 + __ffs(mover) - 1 : -1;
+        const int i = i0 + u * kNT;
+        j[u] = i < movers ? mover_slot[i] : -1;
         if (j[u] < 0) continue;
-        mover &= mover - 1;
-        to[u] = __ldcg(&p.from_slot[row + n_new + mover_at++]);
+        to[u] = __ldcg(&list[mover_at + i]);
         if (p.weights_out) x[u] = w[j[u]];
         if (p.pos_out) q[u] = pos[j[u]];
       }
@@ -632,7 +645,7 @@ cudaError_t launch_evict_plan(const va_evict_args& a, int sms, cudaStream_t st) 
   const bool held = run <= kMaxRun;
   const int bytes = held ? kNT * run * 4 + kNT * run / 8 + 4 : slots / kVec;
   auto* kernel = held ? evict_plan_kernel<true> : evict_plan_kernel<false>;
-  if (bytes > 24 * 1024) {  // past the default limit, beside the static arrays
+  if (bytes > 20 * 1024) {  // past the default limit, beside the static arrays
     static std::atomic<bool> done[2][kMaxDevices];
     cudaError_t e = raise_smem_once(
         kernel, held ? kNT * kMaxRun * 4 + kNT * kMaxRun / 8 + 4 : kMaxKeepBytes, done[held]);
