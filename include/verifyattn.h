@@ -431,8 +431,10 @@ size_t va_key_weights_workspace_bytes(const va_key_weight_args* args);
  * for 0 <= j < kv_len[b]; entries from kv_len[b] on are not touched.  A node
  * counts as often as path lists it; rows whose own mask bit is clear or whose
  * lse is -inf (absent nodes) add nothing.  Products of bf16 queries run on
- * tensor cores unless VA_FLAG_BF16_CUDA_CORES is given; sums are fp32, and
- * their order, so every bit of the result, depends on sizes alone.
+ * tensor cores unless VA_FLAG_BF16_CUDA_CORES is given (queries over an FP8
+ * cache as sums of three E5M2 numbers, exact to 2^-31 of a row's largest
+ * element; a row with an infinity or NaN gives NaN); sums are fp32, and their
+ * order, so every bit of the result, depends on sizes alone.
  * req_status[b] becomes VA_ERR_INVALID_ARG when kv_len[b] is out of range
  * (the request's weights are then not written), when accept_len[b] is outside
  * [0, T] (nothing is added), or when a path entry or a page index is out of
@@ -512,8 +514,8 @@ int va_kv_move(void* c_kv, void* k_pe, int elem_bytes, int num_pages, int page_s
 
 /*
  * Diagnostic: number of bounded barrier waits inside the attention kernels
- * (the tensor-core kernel's pipeline barriers, the CUDA-core kernel's
- * bulk-copy staging of an fp32 cache) that expired on the current device
+ * (the tensor-core kernels' pipeline barriers, va_key_weights' among
+ * them, and the CUDA-core kernel's bulk-copy staging of an fp32 cache) that expired on the current device
  * since the library was loaded (each expiry also flags its request with
  * VA_ERR_CUDA).  Synchronises the
  * device; returns 0xFFFFFFFF if the counter cannot be read.

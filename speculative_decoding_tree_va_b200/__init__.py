@@ -313,8 +313,7 @@ def verify_attn_partials(args: VaAttnArgs, split_first: int, split_count: int, o
     lse_part float [count, B, T, H] (cuda tensors), no merge."""
     _check(load_library().va_verify_attn_partials(ctypes.byref(args), split_first, split_count,
                                                   _ptr(o_part), _ptr(lse_part), _stream(stream)),
-           "va_verify_attn_partials", "va_token_logprobs", "va_key_weights_workspace_bytes",
-           "va_key_weights", "va_evict_plan", "va_kv_move")
+           "va_verify_attn_partials")
 
 
 def merge(o_part, lse_part, out_dtype, stream=None):

@@ -184,6 +184,14 @@ def test_flagged_requests(va, dtype, kv, flags):
     assert off.max() <= RTOL
 
 
+@pytest.mark.parametrize("flags", [0, 1])
+def test_many_short_requests(va, flags):
+    """More requests than the kernel has threads: its ranges begin inside a thread's share."""
+    rng = np.random.default_rng(21)
+    c = Case(22, 1100, 2, 3, rng.integers(0, 40, 1100), "bf16")
+    near(c.run(va, flags=flags), c.ref())
+
+
 def test_empty_counts(va):
     """No accepted node, and a path that lists a node twice."""
     c = Case(8, 2, 4, 9, (100, 30))
