@@ -133,17 +133,17 @@ int check_key_weights(const va_key_weight_args* a) {
   return VA_OK;
 }
 
-// Row splits of a key-weight call (grid z).  A CTA's work is its key tile
-// times its share of the row blocks; rows are split while the key tiles alone
-// would leave SMs idle.  With an accepted path the host does not know its
-// length: a path of the deepest tree is assumed, and splits without rows only
-// write zeros.
 bool key_weights_on_tc(const va_key_weight_args* a) {
   return a->dtype == VA_BF16 && !(a->flags & VA_FLAG_BF16_CUDA_CORES);
 }
 
+// Row splits of a key-weight call; on CUDA cores (grid z) a CTA's work is its key tile
+// times its share of the row blocks; rows are split while the key tiles alone
+// would leave SMs idle.  With an accepted path the host does not know its
+// length: a path of the deepest tree is assumed, and splits without rows only
+// write zeros.
 int key_weight_splits(const va_key_weight_args* a) {
-  if (key_weights_on_tc(a)) return 1;
+  if (key_weights_on_tc(a)) return va::kweights_tc_splits(*a, sm_count());
   const int sms = sm_count();
   const int nodes = a->path && a->T > VA_MAX_DEPTH + 1 ? VA_MAX_DEPTH + 1 : a->T;
   const long long blocks = ((long long)nodes * a->H + va::kKwRows - 1) / va::kKwRows;
@@ -155,10 +155,14 @@ int key_weight_splits(const va_key_weight_args* a) {
   return s < 1 ? 1 : (int)s;
 }
 
+// Workspace of a call: the tensor-core kernel's rows, then the splits' sums.
+size_t key_weight_rows(const va_key_weight_args* a) {
+  return key_weights_on_tc(a) ? va::align256(va::kweights_tc_workspace(*a)) : 0;
+}
 size_t key_weight_workspace(const va_key_weight_args* a, int splits) {
-  if (key_weights_on_tc(a)) return va::kweights_tc_workspace(*a);
-  if (splits < 2) return 0;
-  return va::align256((size_t)splits * a->B * a->max_pages * VA_PAGE_SIZE * sizeof(float));
+  if (splits < 2) return key_weight_rows(a);
+  return key_weight_rows(a) +
+         va::align256((size_t)splits * a->B * a->max_pages * VA_PAGE_SIZE * sizeof(float));
 }
 
 }  // namespace
@@ -394,7 +398,9 @@ int va_key_weights(const va_key_weight_args* args, va_stream_t stream) {
   p.accept_len = args->accept_len;
   p.weights_in = args->weights_in;
   p.weights = args->weights;
-  p.part = splits > 1 ? static_cast<float*>(args->workspace) : nullptr;
+  p.part = splits > 1 ? reinterpret_cast<float*>(static_cast<char*>(args->workspace) +
+                                                  key_weight_rows(args))
+                      : nullptr;
   p.req_status = args->req_status;
   p.B = args->B;
   p.H = args->H;

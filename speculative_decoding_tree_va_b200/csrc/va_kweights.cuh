@@ -101,8 +101,9 @@ __device__ __forceinline__ void kw_store(const KwParams& p, int b, int split, in
 
 cudaError_t launch_kweights_simt(const va_key_weight_args& a, const KwParams& p, cudaStream_t st);
 cudaError_t launch_kweights_join(const KwParams& p, cudaStream_t st);
-// The tensor-core kernel: no splits; its workspace holds the counted rows
-// where they must be laid out or converted first.
+// The tensor-core kernel.  Its workspace holds the counted rows where they must be
+// laid out or converted first; the partial sums follow.
+int kweights_tc_splits(const va_key_weight_args& a, int sms);
 size_t kweights_tc_workspace(const va_key_weight_args& a);
 cudaError_t launch_kweights_tc(const va_key_weight_args& a, const KwParams& p, int sms,
                                cudaStream_t st);

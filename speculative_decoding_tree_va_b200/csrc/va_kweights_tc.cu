@@ -142,7 +142,16 @@ struct Shape {
   }
 };
 
-// The pair's tiles, in order.  Every warp role walks them by itself.
+// Tiles of a request, each in `splits` parts, and what a part costs.
+__device__ __forceinline__ int part_count(int kv_len, int splits) {
+  return (kv_len + kTileKeys - 1) / kTileKeys * splits;
+}
+template <bool F8>
+__device__ __forceinline__ int part_cost(const Shape<F8>& sh, int splits) {
+  return max(1, sh.cost() / splits);
+}
+
+// The pair's tiles (parts of tiles), in order.  Every warp role walks them by itself.
 template <bool F8>
 struct Walk {
   const KwParams* p;
@@ -150,6 +159,18 @@ struct Walk {
   int b, tile, tiles, R, kv_len, cost;
   KwRequest rq;
   Shape<F8> sh;
+  int at, part, rb0, rb1;  // key tile, its part, and that one's row blocks
+  __device__ __forceinline__ void place() {
+    at = tile;
+    part = rb0 = 0;
+    rb1 = sh.blocks;
+    if (p->splits > 1) {
+      at = tile / p->splits;
+      part = tile - at * p->splits;
+      rb0 = sh.blocks * part / p->splits;
+      rb1 = sh.blocks * (part + 1) / p->splits;
+    }
+  }
   __device__ __forceinline__ void load() {
     for (; b < p->B; ++b) {
       rq = kw_request(*p, b);
@@ -157,10 +178,11 @@ struct Walk {
     }
     if (b < p->B) {
       kv_len = rq.kv_len;
-      tiles = (kv_len + kTileKeys - 1) / kTileKeys;
       R = rq.nodes * p->H;
       sh.set(R);
-      cost = sh.cost();
+      tiles = part_count(kv_len, p->splits);
+      cost = part_cost(sh, p->splits);
+      place();
     }
   }
   __device__ __forceinline__ void start(const KwParams& kp, const Ctl& c) {
@@ -178,6 +200,8 @@ struct Walk {
       ++b;
       tile = 0;
       load();
+    } else {
+      place();
     }
   }
   // no later tile of this pair belongs to this request
@@ -256,8 +280,8 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
     auto tiles_cost = [&](const KwRequest& rq, int* tiles) {
       Shape<F8> sh;
       sh.set(rq.nodes * p.H);
-      *tiles = (rq.kv_len + kTileKeys - 1) / kTileKeys;
-      return sh.cost();
+      *tiles = part_count(rq.kv_len, p.splits);
+      return part_cost(sh, p.splits);
     };
     long long sum = 0;
     for (int b = b0; b < b1; ++b) {
@@ -342,7 +366,8 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
     const int oob = p.num_pages * kPage;  // past the pool: zeros
     for (; w.alive() && go; w.next()) {
       if (new_request(go)) ring.restart(w.sh.k_slots());
-      const int key = w.tile * kTileKeys + (int)rank * 128;
+      if (w.rb0 == w.rb1) continue;  // a part without row blocks
+      const int key = w.at * kTileKeys + (int)rank * 128;
       int r0 = kw_pool_row(p, w.b, w.kv_len, key);
       int r1 = kw_pool_row(p, w.b, w.kv_len, key + kPage);
       r0 = r0 < 0 ? oob : r0;
@@ -393,26 +418,28 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
       while (box > 0 && ((half | tp.run) & ((8 << box) - 1))) --box;
       const int box_rows = 8 << box;
       const bool mine = lane < half / box_rows;
-      for (int rb = 0; rb < w.sh.blocks && go; ++rb) {
-        const int y = mine ? map_row(rb * w.sh.cols + (int)rank * half + lane * box_rows) : 0;
-        // this lane's boxes of a chunk, one a plane
-        auto boxes = [&](int kc, uint8_t* at, uint32_t bar) {
-          const bool pe = kc == Ch::n - 1;
-          const int wide = Ch::width(kc), e = F8 ? 1 : 2;
-          for (int pl = 0; pl < Ch::planes; ++pl)
-            tma_2d(smem_u32(at + (pl * half + lane * box_rows) * wide),
-                   pe ? &tm_q.pe[box] : &tm_q.nope[box], bar,
-                   pl * (pe ? kDr : kDc) + (pe ? 0 : kc * (128 / e)), y);
-        };
-        if (w.sh.stay) {  // all chunks at once
-          if (lane == 0 && rank == 0) arrive_expect_tx(&c.r_full, 2 * w.sh.rows_stay());
-          __syncwarp();
-          const uint32_t bar = map_to_rank(smem_u32(&c.r_full), 0);
-          if (mine)
-            for (int kc = 0; kc < Ch::n; ++kc) boxes(kc, sm + w.sh.q_at() + kc * w.sh.q_slot(), bar);
-          __syncwarp();
-          continue;
+      // this lane's boxes of a chunk, one a plane
+      auto boxes = [&](int kc, uint8_t* at, uint32_t bar, int y) {
+        const bool pe = kc == Ch::n - 1;
+        const int wide = Ch::width(kc), e = F8 ? 1 : 2;
+        for (int pl = 0; pl < Ch::planes; ++pl)
+          tma_2d(smem_u32(at + (pl * half + lane * box_rows) * wide),
+                 pe ? &tm_q.pe[box] : &tm_q.nope[box], bar,
+                 pl * (pe ? kDr : kDc) + (pe ? 0 : kc * (128 / e)), y);
+      };
+      if (w.sh.stay) {  // all chunks at once
+        if (lane == 0 && rank == 0) arrive_expect_tx(&c.r_full, 2 * w.sh.rows_stay());
+        __syncwarp();
+        const uint32_t bar = map_to_rank(smem_u32(&c.r_full), 0);
+        if (mine) {
+          const int y = map_row((int)rank * half + lane * box_rows);
+          for (int kc = 0; kc < Ch::n; ++kc) boxes(kc, sm + w.sh.q_at() + kc * w.sh.q_slot(), bar, y);
         }
+        __syncwarp();
+        continue;
+      }
+      for (int rb = w.rb0; rb < w.rb1 && go; ++rb) {
+        const int y = mine ? map_row(rb * w.sh.cols + (int)rank * half + lane * box_rows) : 0;
         for (int kc = 0; kc < Ch::n && go; ++kc) {
           const int s = ring.slot;
           go = wait(&c.q_empty[s], ring.phase() ^ 1);
@@ -421,7 +448,7 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
             arrive_expect_tx(&c.q_full[s], w.sh.cols * Ch::planes * Ch::width(kc));
           __syncwarp();
           if (mine)
-            boxes(kc, sm + w.sh.q_at() + s * w.sh.q_slot(), map_to_rank(smem_u32(&c.q_full[s]), 0));
+            boxes(kc, sm + w.sh.q_at() + s * w.sh.q_slot(), map_to_rank(smem_u32(&c.q_full[s]), 0), y);
           __syncwarp();
           ring.advance();
         }
@@ -455,14 +482,18 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
         const int q_slot = w.sh.q_slot(), half = w.sh.cols / 2;
         const bool seg_end = w.last_of_request();
         const Ring first = kring;  // the tile's first chunk: every block begins there
-        for (int rb = 0; rb < w.sh.blocks && ok; ++rb, ++pass) {
+        if (w.rb0 == w.rb1 && seg_end && ok) {  // nothing to multiply, but the request ends
+          if (elect_one()) commit_pair(&c.seg_done);
+          __syncwarp();
+        }
+        for (int rb = w.rb0; rb < w.rb1 && ok; ++rb, ++pass) {
           const uint32_t d = tmem + (pass & 1) * 256;
-          const bool last = rb == w.sh.blocks - 1;
-          if (rb > 0) kring = first;
+          const bool last = rb == w.rb1 - 1;
+          if (rb > w.rb0) kring = first;
           ok = wait(&c.s_empty[pass & 1], ((pass >> 1) & 1) ^ 1);
           for (int kc = 0; kc < Ch::n && ok; ++kc) {
             const int ks = kring.slot, qs = qring.slot;
-            if (rb == 0) ok = wait(&c.k_full[ks], kring.phase());
+            if (rb == w.rb0) ok = wait(&c.k_full[ks], kring.phase());
             if (ok && stream) ok = wait(&c.q_full[qs], qring.phase());
             if (!ok) break;
             if (elect_one()) {
@@ -516,7 +547,7 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
     uint32_t pass = 0;
     bool go = true;
     for (; w.alive() && go; w.next()) {
-      for (int rb = 0; rb < w.sh.blocks && go; ++rb, ++pass) {
+      for (int rb = w.rb0; rb < w.rb1 && go; ++rb, ++pass) {
         const int buf = pass & 1;
         if (buf != warp - kWarpInfo) continue;
         bool free = false;
@@ -573,13 +604,15 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
     const int W = (p.T + 63) >> 6;
     uint32_t pass = 0, tile_no = 0;
     for (; w.alive(); w.next(), ++tile_no) {
-      const int key = w.tile * kTileKeys + (int)rank * 128 + m;
+      const int key = w.at * kTileKeys + (int)rank * 128 + m;
       const int krow = half == 0 ? kw_pool_row(p, w.b, w.kv_len, key) : 0;
       const size_t slot = (size_t)w.b * p.max_pages * kPage + key;
-      const float old = half == 0 && p.weights_in && key < w.kv_len ? p.weights_in[slot] : 0.f;
+      const float old =
+          half == 0 && p.splits == 1 && p.weights_in && key < w.kv_len ? p.weights_in[slot] : 0.f;
       const int P = w.kv_len - p.T;
       // a tail key is seen by some nodes only: bit n of (seen0, seen1) for node n
-      const bool tail = w.tile * kTileKeys + (int)rank * 128 + 32 * q + 32 > P;  // of the warp
+      const bool tail =  // of the warp
+          w.at * kTileKeys + (int)rank * 128 + 32 * q + 32 > P && w.rb0 < w.rb1;
       const int nd = key - P;
       uint64_t seen0 = ~0ull, seen1 = ~0ull;
       if (tail && nd >= 0) {
@@ -596,7 +629,7 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
       };
       const int cols = w.sh.cols / 2, c0 = half * cols;  // this half's: a multiple of 32
       float sum[4] = {0.f, 0.f, 0.f, 0.f};
-      for (int rb = 0; rb < w.sh.blocks; ++rb, ++pass) {
+      for (int rb = w.rb0; rb < w.rb1; ++rb, ++pass) {
         const int buf = pass & 1;
         const uint32_t parity = (pass >> 1) & 1;
         wait(&c.i_full[buf], parity);
@@ -653,7 +686,9 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
       if (half == 1) c.xsum[tile_no & 1][m] = s;
       asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");
       if (half == 0 && key < w.kv_len) {
-        p.weights[slot] = p.decay * old + (krow >= 0 ? s + c.xsum[tile_no & 1][m] : 0.f);
+        const float all = krow >= 0 ? s + c.xsum[tile_no & 1][m] : 0.f;
+        if (p.splits == 1) p.weights[slot] = p.decay * old + all;
+        else p.part[(size_t)w.part * p.B * p.max_pages * kPage + slot] = all;
         if (krow < 0 && p.req_status) p.req_status[w.b] = VA_ERR_INVALID_ARG;
         if (*abort && p.req_status) p.req_status[w.b] = VA_ERR_CUDA;
       }
@@ -762,6 +797,28 @@ bool needs_rows(const va_key_weight_args& a) {
 
 }  // namespace
 
+// Parts of a tile: two of them a pair where there are fewer tiles than pairs, while
+// there are row blocks for it (as the host sees them: an accepted path of the
+// deepest tree at most).  33 against 21 us for 9 tiles of 9 blocks, 53 against 27
+// for 5 of 17, 94 against 69 for 32 of 33; with a tile a pair and more the keys'
+// second loads cost more than the even shares give (238 against 260 for 272 of 17).
+int kweights_tc_splits(const va_key_weight_args& a, int sms) {
+  const long long nodes = a.path && a.T > VA_MAX_DEPTH + 1 ? VA_MAX_DEPTH + 1 : a.T;
+  const long long rows = nodes * a.H;
+  const bool f8 = a.flags & VA_FLAG_KV_FP8_E4M3;
+  const int stay = f8 ? Shape<true>::kStay : Shape<false>::kStay;
+  const int pass = f8 ? Shape<true>::kPass : Shape<false>::kPass;
+  if (rows <= stay) return 1;
+  const long long blocks = (rows + pass - 1) / pass;
+  const long long tiles = (long long)a.B * (((long long)a.max_pages * kPage + kTileKeys - 1) / kTileKeys);
+  const long long pairs = sms / 2;
+  if (tiles >= pairs) return 1;
+  long long s = (2 * pairs + tiles - 1) / tiles;
+  if (s > blocks) s = blocks;
+  if (s > VA_MAX_SPLITS) s = VA_MAX_SPLITS;
+  return s < 1 ? 1 : (int)s;
+}
+
 size_t kweights_tc_workspace(const va_key_weight_args& a) {
   return needs_rows(a) ? rows_layout(a, a.flags & VA_FLAG_KV_FP8_E4M3).total : 0;
 }
@@ -806,7 +863,7 @@ cudaError_t launch_kweights_tc(const va_key_weight_args& a, const KwParams& p, i
       !encode_rows(&tkpe, a.k_pe, pool, kDr * (f8 ? 1 : 2), kPage, f8 ? 64 : 128, f8))
     return cudaErrorInvalidValue;
   const long long tiles = (long long)a.B * (((long long)a.max_pages * kPage + kTileKeys - 1) / kTileKeys);
-  const int pairs = (int)(tiles < sms / 2 ? tiles : sms / 2);
+  const int pairs = (int)(tiles * p.splits < sms / 2 ? tiles * p.splits : sms / 2);
   auto* k = f8 ? kweights_tc_kernel<true> : kweights_tc_kernel<false>;
   static std::atomic<bool> done[2][kMaxDevices];
   cudaError_t e = raise_smem_once(k, (int)kSmemBytes, done[f8]);
