@@ -13,7 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from contextlib import ExitStack, nullcontext
+from contextlib import ExitStack
 from typing import Any, NamedTuple, Optional
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -334,14 +334,9 @@ def merge(o_part, lse_part, out_dtype, stream=None):
 # library checks the rest.  What they allocate belongs to the stream that
 # they run on.
 
-_NOWHERE = nullcontext()
-
-
 def _on(t, stream):
     """Context in which t's device and the given stream are the current ones."""
     import torch
-    if stream is None and t.get_device() == torch.cuda.current_device():
-        return _NOWHERE
     if stream is not None and stream.device != t.device:
         raise VerifyAttnError(f"stream of {stream.device} for tensors on {t.device}")
     ctx = ExitStack()
@@ -402,6 +397,9 @@ def token_logprobs(logits, tokens=None, *, k: int = 0, scale: float = 1.0, wide:
     k = int(k)
     if not 0 <= k <= 16:
         raise VerifyAttnError("k is not in 0 .. 16")
+    if stream is not None or dev != torch.cuda.current_device():
+        with _on(logits, stream):
+            return token_logprobs(logits, tokens, k=k, scale=scale, wide=wide, row_status=row_status)
     lead, V = logits.shape[:-1], logits.shape[-1]
     R = lead.numel()
     a = VaLogprobArgs()
@@ -421,29 +419,28 @@ def token_logprobs(logits, tokens=None, *, k: int = 0, scale: float = 1.0, wide:
         a.logits = logits.data_ptr()
     a.dtype = VA_F32 if logits.dtype is f32 else VA_BF16
     a.R, a.V, a.K, a.scale = R, V, k, float(scale)
-    with _on(logits, stream):
-        lse = torch.empty(lead, device=logits.device, dtype=f32)
-        entropy = torch.empty_like(lse)
-        a.lse, a.entropy = lse.data_ptr(), entropy.data_ptr()
-        tok_lp = top_ids = top_lp = None
-        if tokens is not None:
-            G = 1 if tokens.shape == lead else tokens.shape[-1] if tokens.dim() else 0
-            a.tokens = _need(tokens, "tokens", dev, i32, lead if tokens.shape == lead else lead + (G,))
-            a.G = G
-            tok_lp = torch.empty_like(tokens, dtype=f32)
-            a.tok_lp = tok_lp.data_ptr()
-        if k:
-            top_ids = torch.empty(lead + (k,), device=logits.device, dtype=i32)
-            top_lp = torch.empty_like(top_ids, dtype=torch.float64 if wide else f32)
-            a.top_ids = top_ids.data_ptr()
-            if wide:
-                a.top_lp64 = top_lp.data_ptr()
-            else:
-                a.top_lp = top_lp.data_ptr()
-        if row_status is not None:
-            a.row_status = _need(row_status, "row_status", dev, i32, lead)
-        _check(load_library().va_token_logprobs(ctypes.byref(a), _raw_stream(dev)),
-               "va_token_logprobs")
+    on = logits.device
+    lse = torch.empty(*lead, device=on, dtype=f32) if lead else torch.empty((), device=on, dtype=f32)
+    entropy = torch.empty_like(lse)
+    a.lse, a.entropy = lse.data_ptr(), entropy.data_ptr()
+    tok_lp = top_ids = top_lp = None
+    if tokens is not None:
+        G = 1 if tokens.shape == lead else tokens.shape[-1] if tokens.dim() else 0
+        a.tokens = _need(tokens, "tokens", dev, i32, lead if tokens.shape == lead else lead + (G,))
+        a.G = G
+        tok_lp = torch.empty_like(tokens, dtype=f32)
+        a.tok_lp = tok_lp.data_ptr()
+    if k:
+        top_ids = torch.empty(*lead, k, device=on, dtype=i32)
+        top_lp = torch.empty_like(top_ids, dtype=torch.float64 if wide else f32)
+        a.top_ids = top_ids.data_ptr()
+        if wide:
+            a.top_lp64 = top_lp.data_ptr()
+        else:
+            a.top_lp = top_lp.data_ptr()
+    if row_status is not None:
+        a.row_status = _need(row_status, "row_status", dev, i32, lead)
+    _check(load_library().va_token_logprobs(ctypes.byref(a), _raw_stream(dev)), "va_token_logprobs")
     return TokenLogprobs(lse, entropy, tok_lp, top_ids, top_lp)
 
 
@@ -465,6 +462,12 @@ def key_weights(q_nope, q_pe, c_kv, k_pe, page_table, kv_len, tree_mask, lse, *,
     dev, dt, i32, f32 = q_nope.get_device(), q_nope.dtype, torch.int32, torch.float32
     if dt is not f32 and dt is not torch.bfloat16:
         raise VerifyAttnError(f"q_nope is {dt}, not float32 or bfloat16")
+    if dev >= 0 and (stream is not None or dev != torch.cuda.current_device()):
+        with _on(q_nope, stream):
+            return key_weights(q_nope, q_pe, c_kv, k_pe, page_table, kv_len, tree_mask, lse,
+                               scale=scale, path=path, accept_len=accept_len, weights=weights,
+                               decay=decay, out=out, workspace=workspace, req_status=req_status,
+                               flags=flags, kv_scale=kv_scale)
     a = VaKeyWeightArgs()
     a.q_nope = _need(q_nope, "q_nope", dev, dt, (B, T, H, D_LATENT))
     a.q_pe = _need(q_pe, "q_pe", dev, dt, (B, T, H, D_ROPE))
@@ -491,20 +494,19 @@ def key_weights(q_nope, q_pe, c_kv, k_pe, page_table, kv_len, tree_mask, lse, *,
     a.num_pages, a.page_size, a.max_pages = n, PAGE_SIZE, m
     a.flags = flags | (VA_FLAG_KV_FP8_E4M3 if fp8 else 0)
     a.kv_scale = float(kv_scale)
-    with _on(q_nope, stream):
-        if out is None:
-            out = torch.zeros(cap, device=q_nope.device, dtype=f32)
-        a.weights = _need(out, "out", dev, f32, cap)
-        lib, ref = load_library(), ctypes.byref(a)
-        need = lib.va_key_weights_workspace_bytes(ref)
-        if need and workspace is None:
-            workspace = torch.empty(need, device=q_nope.device, dtype=torch.uint8)
-        if workspace is not None:
-            if workspace.get_device() != dev or not workspace.is_contiguous():
-                raise VerifyAttnError("the workspace is not a dense tensor of the same device")
-            a.workspace = workspace.data_ptr()
-            a.workspace_bytes = workspace.numel() * workspace.element_size()
-        _check(lib.va_key_weights(ref, _raw_stream(dev)), "va_key_weights")
+    if out is None:
+        out = torch.zeros(cap, device=q_nope.device, dtype=f32)
+    a.weights = _need(out, "out", dev, f32, cap)
+    lib, ref = load_library(), ctypes.byref(a)
+    need = lib.va_key_weights_workspace_bytes(ref)
+    if need and workspace is None:
+        workspace = torch.empty(need, device=q_nope.device, dtype=torch.uint8)
+    if workspace is not None:
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise VerifyAttnError("the workspace is not a dense tensor of the same device")
+        a.workspace = workspace.data_ptr()
+        a.workspace_bytes = workspace.numel() * workspace.element_size()
+    _check(lib.va_key_weights(ref, _raw_stream(dev)), "va_key_weights")
     return out
 
 
@@ -531,6 +533,11 @@ def evict_plan(weights, kv_len, budget, *, path=None, accept_len=None, tree_len:
     if weights.dim() != 2:
         raise VerifyAttnError("weights are not [B, capacity]")
     dev, i32, f32 = weights.get_device(), torch.int32, torch.float32
+    if dev >= 0 and (stream is not None or dev != torch.cuda.current_device()):
+        with _on(weights, stream):
+            return evict_plan(weights, kv_len, budget, path=path, accept_len=accept_len,
+                              tree_len=tree_len, pos=pos, n_sink=n_sink, n_recent=n_recent,
+                              weights_out=weights_out, pos_out=pos_out, req_status=req_status)
     B, cap = weights.shape
     a = VaEvictArgs()
     a.B, a.capacity, a.T, a.n_sink, a.n_recent = B, cap, tree_len, n_sink, n_recent
@@ -547,20 +554,19 @@ def evict_plan(weights, kv_len, budget, *, path=None, accept_len=None, tree_len:
         raise VerifyAttnError("pos_out without pos")
     if req_status is not None:
         a.req_status = _need(req_status, "req_status", dev, i32, (B,))
-    with _on(weights, stream):
-        new_len = torch.empty_like(kv_len)
-        from_slot = torch.empty_like(weights, dtype=i32)
-        a.new_len, a.from_slot = new_len.data_ptr(), from_slot.data_ptr()
-        if weights_out is None:
-            weights_out = torch.empty_like(weights)
-            a.weights_out = weights_out.data_ptr()
-        else:
-            a.weights_out = _need(weights_out, "weights_out", dev, f32, (B, cap))
-        if pos is not None:
-            if pos_out is None:
-                pos_out = torch.empty_like(pos)
-            a.pos_out = _need(pos_out, "pos_out", dev, i32, (B, cap))
-        _check(load_library().va_evict_plan(ctypes.byref(a), _raw_stream(dev)), "va_evict_plan")
+    new_len = torch.empty_like(kv_len)
+    from_slot = torch.empty_like(weights, dtype=i32)
+    a.new_len, a.from_slot = new_len.data_ptr(), from_slot.data_ptr()
+    if weights_out is None:
+        weights_out = torch.empty_like(weights)
+        a.weights_out = weights_out.data_ptr()
+    else:
+        a.weights_out = _need(weights_out, "weights_out", dev, f32, (B, cap))
+    if pos is not None:
+        if pos_out is None:
+            pos_out = torch.empty_like(pos)
+        a.pos_out = _need(pos_out, "pos_out", dev, i32, (B, cap))
+    _check(load_library().va_evict_plan(ctypes.byref(a), _raw_stream(dev)), "va_evict_plan")
     return EvictPlan(new_len, from_slot, weights_out, pos_out)
 
 
@@ -577,12 +583,14 @@ def kv_move(c_kv, k_pe, page_table, from_slot, new_len, *, req_status=None, stre
         raise VerifyAttnError(f"c_kv is {c_kv.dtype}: not a cache type")
     if B == 0:
         return
+    if dev >= 0 and (stream is not None or dev != torch.cuda.current_device()):
+        with _on(c_kv, stream):
+            return kv_move(c_kv, k_pe, page_table, from_slot, new_len, req_status=req_status)
     c = _need(c_kv, "c_kv", dev, c_kv.dtype, (n, PAGE_SIZE, D_LATENT))
     k = _need(k_pe, "k_pe", dev, c_kv.dtype, (n, PAGE_SIZE, D_ROPE))
     t = _need(page_table, "page_table", dev, i32, (B, m))
     f = _need(from_slot, "from_slot", dev, i32, (B, m * PAGE_SIZE))
     l = _need(new_len, "new_len", dev, i32, (B,))
     s = None if req_status is None else _need(req_status, "req_status", dev, i32, (B,))
-    with _on(c_kv, stream):
-        _check(load_library().va_kv_move(c, k, c_kv.element_size(), n, PAGE_SIZE, t, B, m, f, l, s,
-                                         _raw_stream(dev)), "va_kv_move")
+    _check(load_library().va_kv_move(c, k, c_kv.element_size(), n, PAGE_SIZE, t, B, m, f, l, s,
+                                     _raw_stream(dev)), "va_kv_move")
