@@ -133,17 +133,13 @@ int check_key_weights(const va_key_weight_args* a) {
   return VA_OK;
 }
 
-bool key_weights_on_tc(const va_key_weight_args* a) {
-  return a->dtype == VA_BF16 && !(a->flags & VA_FLAG_BF16_CUDA_CORES);
-}
-
 // Row splits of a key-weight call; on CUDA cores (grid z) a CTA's work is its key tile
 // times its share of the row blocks; rows are split while the key tiles alone
 // would leave SMs idle.  With an accepted path the host does not know its
 // length: a path of the deepest tree is assumed, and splits without rows only
 // write zeros.
 int key_weight_splits(const va_key_weight_args* a) {
-  if (key_weights_on_tc(a)) return va::kweights_tc_splits(*a, sm_count());
+  if (va::kweights_on_tc(*a)) return va::kweights_tc_splits(*a, sm_count());
   const int sms = sm_count();
   const int nodes = a->path && a->T > VA_MAX_DEPTH + 1 ? VA_MAX_DEPTH + 1 : a->T;
   const long long blocks = ((long long)nodes * a->H + va::kKwRows - 1) / va::kKwRows;
@@ -157,7 +153,7 @@ int key_weight_splits(const va_key_weight_args* a) {
 
 // Workspace of a call: the tensor-core kernel's rows, then the splits' sums.
 size_t key_weight_rows(const va_key_weight_args* a) {
-  return key_weights_on_tc(a) ? va::align256(va::kweights_tc_workspace(*a)) : 0;
+  return va::kweights_on_tc(*a) ? va::align256(va::kweights_tc_workspace(*a)) : 0;
 }
 size_t key_weight_workspace(const va_key_weight_args* a, int splits) {
   if (splits < 2) return key_weight_rows(a);
@@ -411,7 +407,7 @@ int va_key_weights(const va_key_weight_args* args, va_stream_t stream) {
   p.scale = (args->flags & VA_FLAG_KV_FP8_E4M3) ? args->scale * args->kv_scale : args->scale;
   p.decay = args->decay;
   cudaError_t e;
-  if (key_weights_on_tc(args)) e = va::launch_kweights_tc(*args, p, sm_count(), (cudaStream_t)stream);
+  if (va::kweights_on_tc(*args)) e = va::launch_kweights_tc(*args, p, sm_count(), (cudaStream_t)stream);
   else e = va::launch_kweights_simt(*args, p, (cudaStream_t)stream);
   if (e == cudaSuccess && splits > 1) e = va::launch_kweights_join(p, (cudaStream_t)stream);
   return e == cudaSuccess ? VA_OK : VA_ERR_CUDA;

@@ -103,6 +103,7 @@ cudaError_t launch_kweights_simt(const va_key_weight_args& a, const KwParams& p,
 cudaError_t launch_kweights_join(const KwParams& p, cudaStream_t st);
 // The tensor-core kernel.  Its workspace holds the counted rows where they must be
 // laid out or converted first; the partial sums follow.
+bool kweights_on_tc(const va_key_weight_args& a);
 int kweights_tc_splits(const va_key_weight_args& a, int sms);
 size_t kweights_tc_workspace(const va_key_weight_args& a);
 cudaError_t launch_kweights_tc(const va_key_weight_args& a, const KwParams& p, int sms,

@@ -1,4 +1,5 @@
-// Key weights on tensor cores (bf16 queries; bf16 or FP8 cache), sm_100a.
+// Key weights on tensor cores, sm_100a: bf16 queries over a bf16 or FP8 cache, and
+// fp32 queries where there is work enough to lay both sides out for it.
 //
 //   w_j = sum over counted rows r, j visible to r, of
 //         exp(scale q_r . k_j - lse_r)
@@ -23,6 +24,12 @@
 // hold the 8 of a bf16, down to 2^-31 of the row's largest element, so three
 // products add up to the exact one; the epilogue undoes the power in fp32.
 //
+// fp32: a number is the sum of three bf16 (8 + 8 + 8 bits).  Two kernels lay queries
+// and cached keys out as such planes; of the nine products those of plane 0 with
+// plane 0 go to one accumulator and the five next larger ones to another, which the
+// epilogue adds in fp32 (the three left out are below 2^-24 of the first).  A chunk's
+// planes of both sides pass through rings, keys again for every row block.
+//
 // Bound by HBM for few rows (1152 or 576 bytes a key) and by the tensor cores
 // for many (128 clocks per 256 x 256 x 16), with the latency of the rings'
 // loads close behind (about 2200 clocks from a slot's release to its refill);
@@ -45,14 +52,17 @@ constexpr int kRegion = 9 * kKSlot + 9 * 64 * 128;  // keys and rows: 216 KB
 constexpr int kWarpK = 0, kWarpMma = 1, kWarpEpi = 2, kWarpQ = 10, kWarpInfo = 11;
 constexpr int kThreads = 13 * 32;     // two warps of column data
 
+enum Mode { kBf16, kFp8, kF32 };
+
 // A row's dims in chunks of 128 bytes: 8 of c_kv and one of k_pe in bf16, 4 of
-// c_kv and half a one of k_pe in FP8; planes: numbers that a query element is the
-// sum of.
-template <bool F8>
+// c_kv and half a one of k_pe in FP8; planes: numbers that an element is the sum of.
+template <int M>
 struct Chunks {
-  static constexpr int n = F8 ? 5 : 9, planes = F8 ? 3 : 1;
-  static constexpr int row_bytes = F8 ? 3 * (kDc + kDr) : 2 * (kDc + kDr);  // of a query row
-  static __device__ __forceinline__ int width(int kc) { return F8 && kc == n - 1 ? 64 : 128; }
+  static constexpr int n = M == kFp8 ? 5 : 9;
+  static constexpr int planes = M == kBf16 ? 1 : 3, k_planes = M == kF32 ? 3 : 1;
+  static constexpr int row_bytes = planes * (M == kFp8 ? 1 : 2) * (kDc + kDr);  // of a query row
+  static constexpr int k_slot = k_planes * kKSlot;
+  static __device__ __forceinline__ int width(int kc) { return M == kFp8 && kc == n - 1 ? 64 : 128; }
 };
 
 struct TcParams {
@@ -112,33 +122,35 @@ __device__ __forceinline__ float ex2f(float x) {
 // Up to kStay rows stay in shared memory: with more, fewer than 6 key chunks
 // would be in flight beside them, which HBM's latency needs (4 slots beside 256
 // rows took 8000 clocks a tile, rows through the ring 5000).
-template <bool F8>
+template <int M>
 struct Shape {
-  using Ch = Chunks<F8>;
-  static constexpr int kStay = F8 ? 128 : 160, kPass = F8 ? 128 : 256;
+  using Ch = Chunks<M>;
+  static constexpr int kStay = M == kFp8 ? 128 : M == kF32 ? -1 : 160, kPass = M == kBf16 ? 256 : 128;
+  static constexpr int kKeySlots = M == kF32 ? 3 : Ch::n;  // when rows pass by
   int blocks, cols;
   bool stay;
   __device__ __forceinline__ void set(int R) {
     stay = R <= kStay;
-    blocks = stay ? 1 : (R + kPass - 1) / kPass;
+    blocks = stay ? 1 : max(1, (R + kPass - 1) / kPass);
     cols = max(64, ((R + blocks - 1) / blocks + 63) & ~63);
   }
   // ring slots, and where keys and rows lie in the region
   __device__ __forceinline__ int rows_stay() const { return cols / 2 * Ch::row_bytes; }
   __device__ __forceinline__ int k_slots() const {
-    return stay ? min(kMaxK, (kRegion - rows_stay()) / kKSlot) : Ch::n;
+    return stay ? min(kMaxK, (kRegion - rows_stay()) / Ch::k_slot) : kKeySlots;
   }
   __device__ __forceinline__ int k_at() const { return stay ? rows_stay() : 0; }
   __device__ __forceinline__ int q_slot() const { return cols / 2 * 128 * Ch::planes; }
   __device__ __forceinline__ int q_slots() const {
-    return min(kMaxQ, (kRegion - Ch::n * kKSlot) / q_slot());
+    return min(kMaxQ, (kRegion - kKeySlots * Ch::k_slot) / q_slot());
   }
-  __device__ __forceinline__ int q_at() const { return stay ? 0 : Ch::n * kKSlot; }
+  __device__ __forceinline__ int q_at() const { return stay ? 0 : kKeySlots * Ch::k_slot; }
   // Clocks of a tile, as measured: few rows wait for the keys' share of HBM, rows
   // through the ring for its latency (5400 a pass of 192 columns, 6500 of 256).
   __device__ __forceinline__ int cost() const {
-    const int column = F8 ? 27 : 18;
-    return stay ? max(F8 ? 3400 : 5400, column * cols + 1000) : blocks * (2200 + column * cols) + 300;
+    const int column = M == kFp8 ? 27 : M == kF32 ? 108 : 18;
+    return stay ? max(M == kFp8 ? 3400 : 5400, column * cols + 1000)
+                : blocks * (2200 + column * cols) + 300;
   }
 };
 
@@ -146,19 +158,19 @@ struct Shape {
 __device__ __forceinline__ int part_count(int kv_len, int splits) {
   return (kv_len + kTileKeys - 1) / kTileKeys * splits;
 }
-template <bool F8>
-__device__ __forceinline__ int part_cost(const Shape<F8>& sh, int splits) {
+template <int M>
+__device__ __forceinline__ int part_cost(const Shape<M>& sh, int splits) {
   return max(1, sh.cost() / splits);
 }
 
 // The pair's tiles (parts of tiles), in order.  Every warp role walks them by itself.
-template <bool F8>
+template <int M>
 struct Walk {
   const KwParams* p;
   long long off, end;
   int b, tile, tiles, R, kv_len, cost;
   KwRequest rq;
-  Shape<F8> sh;
+  Shape<M> sh;
   int at, part, rb0, rb1;  // key tile, its part, and that one's row blocks
   __device__ __forceinline__ void place() {
     at = tile;
@@ -223,11 +235,12 @@ struct Ring {
   }
 };
 
-template <bool F8>
+template <int M>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ CUtensorMap tm_ckv,
                    const __grid_constant__ CUtensorMap tm_kpe, const __grid_constant__ TcParams tp) {
-  using Ch = Chunks<F8>;
+  using Ch = Chunks<M>;
+  constexpr bool F8 = M == kFp8, F32 = M == kF32;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
   Ctl& c = *reinterpret_cast<Ctl*>(sm + kRegion);
@@ -278,7 +291,7 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
     const int q = (p.B + kThreads - 1) / kThreads;
     const int b0 = min(p.B, tid * q), b1 = min(p.B, b0 + q);
     auto tiles_cost = [&](const KwRequest& rq, int* tiles) {
-      Shape<F8> sh;
+      Shape<M> sh;
       sh.set(rq.nodes * p.H);
       *tiles = part_count(rq.kv_len, p.splits);
       return part_cost(sh, p.splits);
@@ -345,7 +358,7 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
   cluster_sync_all();
   fence_after();
   const uint32_t tmem = c.tmem;
-  Walk<F8> w;
+  Walk<M> w;
   w.start(p, c);
   // Every role that touches the region begins a request's tiles alike: it waits
   // until the pair's last request there is multiplied, for its layout goes.
@@ -363,32 +376,45 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
     // ------------------------------------------------------------- key chunks by TMA
     bool go = true;
     Ring ring;
-    const int oob = p.num_pages * kPage;  // past the pool: zeros
+    const int oob = (F32 ? p.B * p.max_pages : p.num_pages) * kPage;  // past the pool: zeros
     for (; w.alive() && go; w.next()) {
       if (new_request(go)) ring.restart(w.sh.k_slots());
       if (w.rb0 == w.rb1) continue;  // a part without row blocks
       const int key = w.at * kTileKeys + (int)rank * 128;
-      int r0 = kw_pool_row(p, w.b, w.kv_len, key);
-      int r1 = kw_pool_row(p, w.b, w.kv_len, key + kPage);
-      r0 = r0 < 0 ? oob : r0;
-      r1 = r1 < 0 ? oob : r1;
-      for (int kc = 0; kc < Ch::n && go; ++kc) {
-        const int s = ring.slot;
-        go = wait(&c.k_empty[s], ring.phase() ^ 1);
-        if (!go) break;
-        if (elect_one()) {
-          const bool pe = kc == Ch::n - 1;
-          const CUtensorMap* map = pe ? &tm_kpe : &tm_ckv;
-          const int x = pe ? 0 : kc * (F8 ? 128 : 64);
-          const int bytes = 128 * Ch::width(kc);
-          const uint32_t bar = map_to_rank(smem_u32(&c.k_full[s]), 0);
-          if (rank == 0) arrive_expect_tx(&c.k_full[s], 2 * bytes);
-          const uint32_t dst = smem_u32(sm + w.sh.k_at() + s * kKSlot);
-          tma_2d(dst, map, bar, x, r0);
-          tma_2d(dst + bytes / 2, map, bar, x, r1);
+      int r0, r1;
+      if (F32) {  // laid out by request and slot
+        const long long at = ((long long)w.b * p.max_pages) * kPage + key;
+        r0 = key < w.kv_len ? (int)at : oob;
+        r1 = key + kPage < w.kv_len ? (int)at + kPage : oob;
+      } else {
+        r0 = kw_pool_row(p, w.b, w.kv_len, key);
+        r1 = kw_pool_row(p, w.b, w.kv_len, key + kPage);
+        r0 = r0 < 0 ? oob : r0;
+        r1 = r1 < 0 ? oob : r1;
+      }
+      for (int rb = F32 ? w.rb0 : w.rb1 - 1; rb < w.rb1 && go; ++rb) {
+        for (int kc = 0; kc < Ch::n && go; ++kc) {
+          const int s = ring.slot;
+          go = wait(&c.k_empty[s], ring.phase() ^ 1);
+          if (!go) break;
+          if (elect_one()) {
+            const bool pe = kc == Ch::n - 1;
+            const CUtensorMap* map = pe ? &tm_kpe : &tm_ckv;
+            const int bytes = 128 * Ch::width(kc);
+            const uint32_t bar = map_to_rank(smem_u32(&c.k_full[s]), 0);
+            if (rank == 0) arrive_expect_tx(&c.k_full[s], 2 * bytes * Ch::k_planes);
+            uint32_t dst = smem_u32(sm + w.sh.k_at() + s * Ch::k_slot);
+            int x = pe ? 0 : kc * (F8 ? 128 : 64);
+            for (int pl = 0; pl < Ch::k_planes; ++pl) {
+              tma_2d(dst, map, bar, x, r0);
+              tma_2d(dst + bytes / 2, map, bar, x, r1);
+              dst += kKSlot;
+              x += pe ? kDr : kDc;
+            }
+          }
+          __syncwarp();
+          ring.advance();
         }
-        __syncwarp();
-        ring.advance();
       }
     }
     // the last use of every slot must be over before the CTA may exit
@@ -489,17 +515,29 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
         for (int rb = w.rb0; rb < w.rb1 && ok; ++rb, ++pass) {
           const uint32_t d = tmem + (pass & 1) * 256;
           const bool last = rb == w.rb1 - 1;
-          if (rb > w.rb0) kring = first;
+          if (rb > w.rb0 && !F32) kring = first;
           ok = wait(&c.s_empty[pass & 1], ((pass >> 1) & 1) ^ 1);
           for (int kc = 0; kc < Ch::n && ok; ++kc) {
             const int ks = kring.slot, qs = qring.slot;
-            if (rb == w.rb0) ok = wait(&c.k_full[ks], kring.phase());
+            if (rb == w.rb0 || F32) ok = wait(&c.k_full[ks], kring.phase());
             if (ok && stream) ok = wait(&c.q_full[qs], qring.phase());
             if (!ok) break;
             if (elect_one()) {
               fence_after();
-              const uint32_t ka = k0 + ks * kKSlot, qa = q0 + (stream ? qs : kc) * q_slot;
-              if (!F8) {
+              const uint32_t ka = k0 + ks * Ch::k_slot, qa = q0 + (stream ? qs : kc) * q_slot;
+              if (F32) {
+                // planes (0, 0) to d; (0, 1), (1, 0), (0, 2), (1, 1), (2, 0) beside it
+#pragma unroll 1
+                for (int i = 0; i < 6; ++i) {
+                  const int pa = (0x210100 >> (4 * i)) & 3, pb = (0x012010 >> (4 * i)) & 3;
+                  const uint64_t a = sw128_desc(ka + pa * kKSlot), b = sw128_desc(qa + pb * half * 128);
+                  const uint32_t to = i ? d + 128 : d;
+                  mma_pair(to, a, b, idesc, kc != 0 || i > 1);
+                  mma_pair(to, a + 2, b + 2, idesc, 1u);
+                  mma_pair(to, a + 4, b + 4, idesc, 1u);
+                  mma_pair(to, a + 6, b + 6, idesc, 1u);
+                }
+              } else if (!F8) {
                 const uint64_t a = sw128_desc(ka), b = sw128_desc(qa);
                 mma_pair(d, a, b, idesc, kc != 0);
                 mma_pair(d, a + 2, b + 2, idesc, 1u);
@@ -521,7 +559,7 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
                 }
               }
               if (stream) commit_pair(&c.q_empty[qs]);
-              if (last) commit_pair(&c.k_empty[ks]);
+              if (last || F32) commit_pair(&c.k_empty[ks]);
               if (kc == Ch::n - 1) {
                 commit_pair(&c.s_full[pass & 1]);
                 if (last && seg_end) commit_pair(&c.seg_done);
@@ -643,7 +681,15 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
         for (int g = 0; g < cols; g += 32) {
           float x[32];
           ld32(scores + g, x);
-          wait_ld();
+          if (F32) {
+            float y[32];
+            ld32(scores + 128 + g, y);
+            wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] += y[i];
+          } else {
+            wait_ld();
+          }
           if (g + 32 == cols) {  // all scores are in registers: the buffer may be written again
             fence_before();
             __syncwarp();
@@ -705,15 +751,79 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
   }
 }
 
+// x as the sum of three bf16 (what is left of it after two has 8 bits).
+__device__ __forceinline__ void split3(float x, __nv_bfloat16 (&o)[3]) {
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    o[i] = __float2bfloat16_rn(x);
+    x -= __bfloat162float(o[i]);
+  }
+}
+__device__ __forceinline__ void load4(const float* p, float (&x)[4]) {
+  const float4 v = *reinterpret_cast<const float4*>(p);
+  x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+}
+__device__ __forceinline__ void load4(const __nv_fp8_e4m3* p, float (&x)[4]) {
+  const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float2 f = __half22float2(__half2(
+        __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(v >> (16 * i)), __NV_E4M3)));
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+// One warp writes a row's planes: [3][512] at row `to` of n, [3][64] of pe.
+template <typename T>
+__device__ __forceinline__ void split_row(const T* nope, const T* rope, size_t to, void* n, void* pe) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < 5; ++i) {  // four elements a lane
+    if (i == 4 && lane >= 16) break;
+    float x[4];
+    load4(i < 4 ? nope + (i * 32 + lane) * 4 : rope + lane * 4, x);
+    __nv_bfloat16 o[4][3];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) split3(x[k], o[k]);
+    uint2* dst = i < 4 ? reinterpret_cast<uint2*>(n) + to * (3 * kDc / 4) + i * 32 + lane
+                       : reinterpret_cast<uint2*>(pe) + to * (3 * kDr / 4) + lane;
+#pragma unroll
+    for (int pl = 0; pl < 3; ++pl) {
+      __nv_bfloat162 lo(o[0][pl], o[1][pl]), hi(o[2][pl], o[3][pl]);
+      dst[pl * (i < 4 ? kDc / 4 : kDr / 4)] =
+          make_uint2(*reinterpret_cast<uint32_t*>(&lo), *reinterpret_cast<uint32_t*>(&hi));
+    }
+  }
+}
+
+// The requests' cached keys as planes of three bf16: slot j of request b is row
+// (b max_pages) 64 + j.  One CTA per page; pages outside the pool are left out.
+template <typename T>
+__global__ void __launch_bounds__(256)
+kweights_keys_kernel(const KwParams p, void* __restrict__ n, void* __restrict__ pe) {
+  const int b = blockIdx.y, page = blockIdx.x, warp = threadIdx.x >> 5;
+  const KwRequest rq = kw_request(p, b);
+  const int key0 = page * kPage;
+  if (!rq.ok || key0 >= rq.kv_len) return;
+  const int row0 = kw_pool_row(p, b, rq.kv_len, key0);
+  if (row0 < 0) return;
+  const int keys = min(kPage, rq.kv_len - key0);
+  for (int r = warp; r < keys; r += 8)
+    split_row(reinterpret_cast<const T*>(p.c_kv) + (size_t)(row0 + r) * kDc,
+              reinterpret_cast<const T*>(p.k_pe) + (size_t)(row0 + r) * kDr,
+              ((size_t)b * p.max_pages + page) * kPage + r, n, pe);
+}
+
 // Counted rows of every request, dense from b * T * H on.  For an FP8 cache each
 // row is multiplied by the power of two that brings its largest element to [2^14,
 // 2^15), and an element x is written as the E5M2 numbers nearest to x, to what is
 // left of it, and to what is left then: planes [3][512] and [3][64] of a row;
 // `scale` gets the inverse power.  One warp per row.
-template <bool F8>
+template <int M>
 __global__ void __launch_bounds__(256)
 kweights_rows_kernel(const KwParams p, uint4* __restrict__ qn, uint4* __restrict__ qp,
                      float* __restrict__ scale) {
+  constexpr bool F8 = M == kFp8;
   const int b = blockIdx.y, lane = threadIdx.x & 31;
   const int r = blockIdx.x * 8 + (threadIdx.x >> 5);
   const KwRequest rq = kw_request(p, b);
@@ -722,6 +832,11 @@ kweights_rows_kernel(const KwParams p, uint4* __restrict__ qn, uint4* __restrict
   const int g = kw_query_row(p, b, rq, r, &node);
   if (g < 0) return;
   const size_t to = (size_t)b * p.T * p.H + r;
+  if (M == kF32) {
+    split_row(reinterpret_cast<const float*>(p.q_nope) + (size_t)g * kDc,
+              reinterpret_cast<const float*>(p.q_pe) + (size_t)g * kDr, to, qn, qp);
+    return;
+  }
   const uint4* sn = reinterpret_cast<const uint4*>(p.q_nope) + (size_t)g * (kDc / 8);
   const uint4* sp = reinterpret_cast<const uint4*>(p.q_pe) + (size_t)g * (kDr / 8);
   uint4 v[3];  // 8 elements each: of q_nope from 8 lane and 256 + 8 lane on, of q_pe from 8 lane
@@ -776,56 +891,89 @@ kweights_rows_kernel(const KwParams p, uint4* __restrict__ qn, uint4* __restrict
   if (lane == 0) scale[to] = ldexpf(1.f, -ex);
 }
 
-struct RowsLayout {
-  size_t qn, qp, scale, total;
+int mode_of(const va_key_weight_args& a) {
+  return a.dtype == VA_F32 ? kF32 : (a.flags & VA_FLAG_KV_FP8_E4M3) ? kFp8 : kBf16;
+}
+struct Layout {
+  size_t qn, qp, scale, kn, kp, total;
 };
-RowsLayout rows_layout(const va_key_weight_args& a, bool f8) {
-  const size_t rows = (size_t)a.B * a.T * a.H;
-  RowsLayout l;
+// Counted rows are laid out densely first when they need converting, or when the
+// accepted nodes' runs of H rows are no whole number of 8-row swizzle groups; fp32
+// keys too, for the pages that the page table can hold.
+bool needs_rows(const va_key_weight_args& a) {
+  return mode_of(a) != kBf16 || (a.path && a.H % 8 != 0);
+}
+Layout layout(const va_key_weight_args& a) {
+  const int m = mode_of(a);
+  const size_t rows = needs_rows(a) ? (size_t)a.B * a.T * a.H : 0;
+  const size_t keys = m == kF32 ? (size_t)a.B * a.max_pages * kPage : 0;
+  const int bytes = m == kFp8 ? 3 : m == kF32 ? 6 : 2;
+  Layout l;
   l.qn = 0;
-  const int bytes = f8 ? 3 : 2;
   l.qp = align256(rows * kDc * bytes);
   l.scale = l.qp + align256(rows * kDr * bytes);
-  l.total = l.scale + (f8 ? align256(rows * sizeof(float)) : 0);
+  l.kn = l.scale + (m == kFp8 ? align256(rows * sizeof(float)) : 0);
+  l.kp = l.kn + align256(keys * kDc * 6);
+  l.total = l.kp + align256(keys * kDr * 6);
   return l;
 }
-// The rows are laid out densely first when they need converting, or when the
-// accepted nodes' runs of H rows are no whole number of 8-row swizzle groups.
-bool needs_rows(const va_key_weight_args& a) {
-  return (a.flags & VA_FLAG_KV_FP8_E4M3) || (a.path && a.H % 8 != 0);
+// Rows of a request as the host sees them: an accepted path of the deepest tree at most.
+long long rows_seen(const va_key_weight_args& a) {
+  const long long nodes = a.path && a.T > VA_MAX_DEPTH + 1 ? VA_MAX_DEPTH + 1 : a.T;
+  return nodes * a.H;
+}
+long long tiles_of(const va_key_weight_args& a) {
+  return (long long)a.B * (((long long)a.max_pages * kPage + kTileKeys - 1) / kTileKeys);
+}
+
+template <int M>
+cudaError_t launch(const QMaps& tq, const CUtensorMap& tckv, const CUtensorMap& tkpe,
+                   const TcParams& tp, int pairs, cudaStream_t st) {
+  static std::atomic<bool> done[kMaxDevices];
+  cudaError_t e = raise_smem_once(kweights_tc_kernel<M>, (int)kSmemBytes, done);
+  if (e != cudaSuccess) return e;
+  kweights_tc_kernel<M><<<2 * pairs, kThreads, kSmemBytes, st>>>(tq, tckv, tkpe, tp);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
+// bf16 queries run here unless the caller asks for CUDA cores; fp32 ones from about
+// 16 us of CUDA-core work on (row blocks of 128 times keys), below which four launches
+// cost more than they save, while the keys' planes (3456 bytes each) stay within 1 GB.
+bool kweights_on_tc(const va_key_weight_args& a) {
+  if (a.flags & VA_FLAG_BF16_CUDA_CORES) return false;
+  if (a.dtype == VA_BF16) return true;
+  const long long rows = (rows_seen(a) + 127) / 128 * 128;
+  const long long keys = (long long)a.B * a.max_pages * kPage;
+  return rows * keys >= (1 << 19) && keys * 6 * kDqk <= (1LL << 30) && keys <= 0x7fffffffLL;
+}
+
 // Parts of a tile: two of them a pair where there are fewer tiles than pairs, while
-// there are row blocks for it (as the host sees them: an accepted path of the
-// deepest tree at most).  33 against 21 us for 9 tiles of 9 blocks, 53 against 27
-// for 5 of 17, 94 against 69 for 32 of 33; with a tile a pair and more the keys'
+// there are row blocks for it.  33 against 21 us for 9 tiles of 9 blocks, 53 against
+// 27 for 5 of 17, 94 against 69 for 32 of 33; with a tile a pair and more the keys'
 // second loads cost more than the even shares give (238 against 260 for 272 of 17).
+// fp32 loads the keys for every block anyway.
 int kweights_tc_splits(const va_key_weight_args& a, int sms) {
-  const long long nodes = a.path && a.T > VA_MAX_DEPTH + 1 ? VA_MAX_DEPTH + 1 : a.T;
-  const long long rows = nodes * a.H;
-  const bool f8 = a.flags & VA_FLAG_KV_FP8_E4M3;
-  const int stay = f8 ? Shape<true>::kStay : Shape<false>::kStay;
-  const int pass = f8 ? Shape<true>::kPass : Shape<false>::kPass;
+  const int m = mode_of(a);
+  const long long rows = rows_seen(a);
+  const int stay = m == kFp8 ? Shape<kFp8>::kStay : m == kF32 ? Shape<kF32>::kStay : Shape<kBf16>::kStay;
+  const int pass = m == kBf16 ? Shape<kBf16>::kPass : Shape<kFp8>::kPass;
   if (rows <= stay) return 1;
-  const long long blocks = (rows + pass - 1) / pass;
-  const long long tiles = (long long)a.B * (((long long)a.max_pages * kPage + kTileKeys - 1) / kTileKeys);
-  const long long pairs = sms / 2;
-  if (tiles >= pairs) return 1;
-  long long s = (2 * pairs + tiles - 1) / tiles;
+  const long long blocks = (rows + pass - 1) / pass, tiles = tiles_of(a), pairs = sms / 2;
+  if (tiles >= (m == kF32 ? 8 : 1) * pairs) return 1;
+  long long s = ((m == kF32 ? 8 : 2) * pairs + tiles - 1) / tiles;
   if (s > blocks) s = blocks;
   if (s > VA_MAX_SPLITS) s = VA_MAX_SPLITS;
   return s < 1 ? 1 : (int)s;
 }
 
-size_t kweights_tc_workspace(const va_key_weight_args& a) {
-  return needs_rows(a) ? rows_layout(a, a.flags & VA_FLAG_KV_FP8_E4M3).total : 0;
-}
+size_t kweights_tc_workspace(const va_key_weight_args& a) { return layout(a).total; }
 
 cudaError_t launch_kweights_tc(const va_key_weight_args& a, const KwParams& p, int sms,
                                cudaStream_t st) {
-  const bool f8 = a.flags & VA_FLAG_KV_FP8_E4M3;
+  const int m = mode_of(a);
+  const bool f8 = m == kFp8;
   const uint64_t rows = (uint64_t)a.B * a.T * a.H;
   TcParams tp;
   tp.k = p;
@@ -833,43 +981,55 @@ cudaError_t launch_kweights_tc(const va_key_weight_args& a, const KwParams& p, i
   tp.run = tp.dense || !a.path ? 64 : a.H;
   tp.q_scale = nullptr;
   tp.scale = (float)((double)p.scale * (1.0 + (f8 ? kShortFp8 : kShortBf16)));
+  const Layout l = layout(a);
+  char* ws = static_cast<char*>(a.workspace);
   const void* qn = a.q_nope;
   const void* qp = a.q_pe;
   if (tp.dense) {
-    const RowsLayout l = rows_layout(a, f8);
-    char* ws = static_cast<char*>(a.workspace);
     qn = ws + l.qn;
     qp = ws + l.qp;
     float* scale = f8 ? reinterpret_cast<float*>(ws + l.scale) : nullptr;
     tp.q_scale = scale;
     const dim3 grid((unsigned)((a.T * a.H + 7) / 8), (unsigned)a.B);
-    auto* k = f8 ? kweights_rows_kernel<true> : kweights_rows_kernel<false>;
+    auto* k = f8 ? kweights_rows_kernel<kFp8>
+                 : m == kF32 ? kweights_rows_kernel<kF32> : kweights_rows_kernel<kBf16>;
     k<<<grid, 256, 0, st>>>(p, (uint4*)qn, (uint4*)qp, scale);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  const void* ckv = a.c_kv;
+  const void* kpe = a.k_pe;
+  uint64_t pool = (uint64_t)a.num_pages * kPage;
+  if (m == kF32) {
+    ckv = ws + l.kn;
+    kpe = ws + l.kp;
+    pool = (uint64_t)a.B * a.max_pages * kPage;
+    const dim3 grid((unsigned)a.max_pages, (unsigned)a.B);
+    auto* k = (a.flags & VA_FLAG_KV_FP8_E4M3) ? kweights_keys_kernel<__nv_fp8_e4m3>
+                                              : kweights_keys_kernel<float>;
+    k<<<grid, 256, 0, st>>>(p, ws + l.kn, ws + l.kp);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
   QMaps tq = {};
   CUtensorMap tckv, tkpe;
-  const uint64_t pool = (uint64_t)a.num_pages * kPage;
+  const int qe = f8 ? 3 : m == kF32 ? 6 : 2, ke = f8 ? 1 : m == kF32 ? 6 : 2;
   // the boxes that halves (multiples of 32 rows) take in these runs: the run's own
   // power of two, and 32 beside 64
   int tallest = kBoxes - 1;
   while (tallest > 0 && tp.run % (8 << tallest)) --tallest;
   for (int i = tallest == kBoxes - 1 ? tallest - 1 : tallest; i <= tallest; ++i)
-    if (!encode_rows(&tq.nope[i], qn, rows, kDc * (f8 ? 3 : 2), 8 << i, 128, f8) ||
-        !encode_rows(&tq.pe[i], qp, rows, kDr * (f8 ? 3 : 2), 8 << i, f8 ? 64 : 128, f8))
+    if (!encode_rows(&tq.nope[i], qn, rows, kDc * qe, 8 << i, 128, f8) ||
+        !encode_rows(&tq.pe[i], qp, rows, kDr * qe, 8 << i, f8 ? 64 : 128, f8))
       return cudaErrorInvalidValue;
-  if (!encode_rows(&tckv, a.c_kv, pool, kDc * (f8 ? 1 : 2), kPage, 128, f8) ||
-      !encode_rows(&tkpe, a.k_pe, pool, kDr * (f8 ? 1 : 2), kPage, f8 ? 64 : 128, f8))
+  if (!encode_rows(&tckv, ckv, pool, kDc * ke, kPage, 128, f8) ||
+      !encode_rows(&tkpe, kpe, pool, kDr * ke, kPage, f8 ? 64 : 128, f8))
     return cudaErrorInvalidValue;
-  const long long tiles = (long long)a.B * (((long long)a.max_pages * kPage + kTileKeys - 1) / kTileKeys);
-  const int pairs = (int)(tiles * p.splits < sms / 2 ? tiles * p.splits : sms / 2);
-  auto* k = f8 ? kweights_tc_kernel<true> : kweights_tc_kernel<false>;
-  static std::atomic<bool> done[2][kMaxDevices];
-  cudaError_t e = raise_smem_once(k, (int)kSmemBytes, done[f8]);
-  if (e != cudaSuccess) return e;
-  k<<<2 * pairs, kThreads, kSmemBytes, st>>>(tq, tckv, tkpe, tp);
-  return cudaGetLastError();
+  const long long parts = tiles_of(a) * p.splits;
+  const int pairs = (int)(parts < sms / 2 ? parts : sms / 2);
+  return f8          ? launch<kFp8>(tq, tckv, tkpe, tp, pairs, st)
+         : m == kF32 ? launch<kF32>(tq, tckv, tkpe, tp, pairs, st)
+                     : launch<kBf16>(tq, tckv, tkpe, tp, pairs, st);
 }
 
 unsigned int kw_timeouts() {

@@ -110,7 +110,7 @@ def near(got, want, what=""):
 
 
 KINDS = [("f32", "f32", 0), ("f32", "fp8", 0), ("bf16", "bf16", 0), ("bf16", "fp8", 0),
-         ("bf16", "bf16", 1), ("bf16", "fp8", 1)]
+         ("bf16", "bf16", 1), ("bf16", "fp8", 1), ("f32", "f32", 1), ("f32", "fp8", 1)]
 
 
 @pytest.mark.parametrize("dtype,kv,flags", KINDS)
