@@ -430,12 +430,13 @@ size_t va_key_weights_workspace_bytes(const va_key_weight_args* args);
  *       exp(scale * (q_nope . c_kv_j + q_pe . k_pe_j) - lse[b][n][h])
  * for 0 <= j < kv_len[b]; entries from kv_len[b] on are not touched.  A node
  * counts as often as path lists it; rows whose own mask bit is clear or whose
- * lse is -inf (absent nodes) add nothing.  Products run on tensor cores (fp32
- * ones as sums of three bf16 on both sides, where there is work enough for it)
- * unless VA_FLAG_BF16_CUDA_CORES is given (queries over an FP8
- * cache as sums of three E5M2 numbers, exact to 2^-31 of a row's largest
- * element; a row with an infinity or NaN gives NaN); sums are fp32, and their
- * order, so every bit of the result, depends on sizes alone.
+ * lse is -inf (absent nodes) add nothing.
+ * Products run on tensor cores: fp32 numbers as sums of three bf16 (while these
+ * take at most 1 GB of workspace for the keys), bf16 queries over an FP8 cache as
+ * sums of three E5M2 numbers, exact to 2^-31 of a row's largest element; rows and
+ * keys with an infinity or NaN give NaN.  With VA_FLAG_BF16_CUDA_CORES, of either
+ * type, they run on CUDA cores.  Sums are fp32, and their order, so every bit of
+ * the result, depends on sizes alone.
  * req_status[b] becomes VA_ERR_INVALID_ARG when kv_len[b] is out of range
  * (the request's weights are then not written), when accept_len[b] is outside
  * [0, T] (nothing is added), or when a path entry or a page index is out of

@@ -1,5 +1,5 @@
-// Key weights on CUDA cores (fp32 queries, or bf16 on request), and the join
-// of row splits that the tensor-core kernel shares.
+// Key weights on CUDA cores (on request, and for the largest fp32 caches), and the
+// join of row splits that the tensor-core kernel shares.
 //
 //   w_j = sum over counted rows r, j visible to r, of
 //         exp(scale q_r . k_j - lse_r)
@@ -194,23 +194,30 @@ __global__ void __launch_bounds__(kThreads, 2) kweights_simt_kernel(const KwPara
 }
 
 // Adds the splits' partial sums, in split order, to the decayed weights.
-__global__ void __launch_bounds__(256) kweights_join_kernel(const KwParams p) {
+__global__ void __launch_bounds__(64) kweights_join_kernel(const KwParams p) {
   const int b = blockIdx.y;
-  const int j = blockIdx.x * 256 + threadIdx.x;
+  const int j = blockIdx.x * 64 + threadIdx.x;
   const KwRequest rq = kw_request(p, b);
   if (!rq.ok || j >= rq.kv_len) return;
   const size_t cap = (size_t)p.max_pages * kPage;
+  const size_t at = (size_t)b * cap + j, step = (size_t)p.B * cap;
+  const float old = p.weights_in ? p.decay * p.weights_in[at] : 0.f;
   float w = 0.f;
-  for (int s = 0; s < p.splits; ++s) w += p.part[((size_t)s * p.B + b) * cap + j];
-  const size_t at = (size_t)b * cap + j;
-  p.weights[at] = (p.weights_in ? p.decay * p.weights_in[at] : 0.f) + w;
+  for (int s0 = 0; s0 < p.splits; s0 += 8) {  // 8 loads in flight, added in order
+    float v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) v[u] = s0 + u < p.splits ? p.part[(s0 + u) * step + at] : 0.f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) w += v[u];
+  }
+  p.weights[at] = old + w;
 }
 
 }  // namespace
 
 cudaError_t launch_kweights_join(const KwParams& p, cudaStream_t st) {
-  const dim3 grid((unsigned)((p.max_pages * kPage + 255) / 256), (unsigned)p.B);
-  kweights_join_kernel<<<grid, 256, 0, st>>>(p);
+  const dim3 grid((unsigned)((p.max_pages * kPage + 63) / 64), (unsigned)p.B);
+  kweights_join_kernel<<<grid, 64, 0, st>>>(p);
   return cudaGetLastError();
 }
 

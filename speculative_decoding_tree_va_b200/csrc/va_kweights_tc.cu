@@ -1,5 +1,5 @@
-// Key weights on tensor cores, sm_100a: bf16 queries over a bf16 or FP8 cache, and
-// fp32 queries where there is work enough to lay both sides out for it.
+// Key weights on tensor cores, sm_100a: bf16 queries over a bf16 or FP8 cache, fp32
+// queries over an fp32 or FP8 cache.
 //
 //   w_j = sum over counted rows r, j visible to r, of
 //         exp(scale q_r . k_j - lse_r)
@@ -797,21 +797,17 @@ __device__ __forceinline__ void split_row(const T* nope, const T* rope, size_t t
 }
 
 // The requests' cached keys as planes of three bf16: slot j of request b is row
-// (b max_pages) 64 + j.  One CTA per page; pages outside the pool are left out.
+// (b max_pages) 64 + j.  One warp per key; keys of pages outside the pool are left out.
 template <typename T>
 __global__ void __launch_bounds__(256)
 kweights_keys_kernel(const KwParams p, void* __restrict__ n, void* __restrict__ pe) {
-  const int b = blockIdx.y, page = blockIdx.x, warp = threadIdx.x >> 5;
+  const int b = blockIdx.y, key = blockIdx.x * 8 + (threadIdx.x >> 5);
   const KwRequest rq = kw_request(p, b);
-  const int key0 = page * kPage;
-  if (!rq.ok || key0 >= rq.kv_len) return;
-  const int row0 = kw_pool_row(p, b, rq.kv_len, key0);
-  if (row0 < 0) return;
-  const int keys = min(kPage, rq.kv_len - key0);
-  for (int r = warp; r < keys; r += 8)
-    split_row(reinterpret_cast<const T*>(p.c_kv) + (size_t)(row0 + r) * kDc,
-              reinterpret_cast<const T*>(p.k_pe) + (size_t)(row0 + r) * kDr,
-              ((size_t)b * p.max_pages + page) * kPage + r, n, pe);
+  const int row = rq.ok ? kw_pool_row(p, b, rq.kv_len, key) : -1;
+  if (row < 0) return;
+  split_row(reinterpret_cast<const T*>(p.c_kv) + (size_t)row * kDc,
+            reinterpret_cast<const T*>(p.k_pe) + (size_t)row * kDr,
+            (size_t)b * p.max_pages * kPage + key, n, pe);
 }
 
 // Counted rows of every request, dense from b * T * H on.  For an FP8 cache each
@@ -938,15 +934,13 @@ cudaError_t launch(const QMaps& tq, const CUtensorMap& tckv, const CUtensorMap& 
 
 }  // namespace
 
-// bf16 queries run here unless the caller asks for CUDA cores; fp32 ones from about
-// 16 us of CUDA-core work on (row blocks of 128 times keys), below which four launches
-// cost more than they save, while the keys' planes (3456 bytes each) stay within 1 GB.
+// Calls run here unless the caller asks for CUDA cores, or fp32 keys' planes (3456
+// bytes each) would take over 1 GB of workspace.  One tile of 128 x 128 takes the
+// CUDA cores about 65 us; a small fp32 call here takes 19 to 27 with its launches.
 bool kweights_on_tc(const va_key_weight_args& a) {
   if (a.flags & VA_FLAG_BF16_CUDA_CORES) return false;
-  if (a.dtype == VA_BF16) return true;
-  const long long rows = (rows_seen(a) + 127) / 128 * 128;
   const long long keys = (long long)a.B * a.max_pages * kPage;
-  return rows * keys >= (1 << 19) && keys * 6 * kDqk <= (1LL << 30) && keys <= 0x7fffffffLL;
+  return a.dtype == VA_BF16 || keys * 6 * kDqk <= (1LL << 30);
 }
 
 // Parts of a tile: two of them a pair where there are fewer tiles than pairs, while
@@ -1004,7 +998,7 @@ cudaError_t launch_kweights_tc(const va_key_weight_args& a, const KwParams& p, i
     ckv = ws + l.kn;
     kpe = ws + l.kp;
     pool = (uint64_t)a.B * a.max_pages * kPage;
-    const dim3 grid((unsigned)a.max_pages, (unsigned)a.B);
+    const dim3 grid((unsigned)(a.max_pages * (kPage / 8)), (unsigned)a.B);
     auto* k = (a.flags & VA_FLAG_KV_FP8_E4M3) ? kweights_keys_kernel<__nv_fp8_e4m3>
                                               : kweights_keys_kernel<float>;
     k<<<grid, 256, 0, st>>>(p, ws + l.kn, ws + l.kp);
