@@ -442,7 +442,7 @@ size_t va_key_weights_workspace_bytes(const va_key_weight_args* args);
  * [0, T] (nothing is added), or when a path entry or a page index is out of
  * range (that node, or that page's keys, get nothing added), and VA_ERR_CUDA
  * when a bounded wait expires (the weights are then unspecified); entries of
- * requests without a problem are not written.
+ * requests without a problem are not written.  T * H over 2^22: VA_ERR_UNSUPPORTED.
  */
 int va_key_weights(const va_key_weight_args* args, va_stream_t stream);
 

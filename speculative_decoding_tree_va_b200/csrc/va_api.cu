@@ -118,8 +118,8 @@ int check_key_weights(const va_key_weight_args* a) {
   if (a->num_pages < 1 || a->max_pages < 1) return VA_ERR_INVALID_ARG;
   if ((long long)a->num_pages * VA_PAGE_SIZE > 0x7fffffffLL ||
       (long long)a->max_pages * VA_PAGE_SIZE > 0x7fffffffLL - VA_SPLIT_ALIGN ||
-      (long long)a->B * a->T * a->H > 0x7fffffffLL)
-    return VA_ERR_UNSUPPORTED;  // pool rows, slots and query rows are 32-bit
+      (long long)a->B * a->T * a->H > 0x7fffffffLL || (long long)a->T * a->H > (1 << 22))
+    return VA_ERR_UNSUPPORTED;  // pool rows, slots, query rows and tile costs are 32-bit
   for (const void* p : {a->q_nope, a->q_pe, a->c_kv, a->k_pe})
     if (!p || !aligned(p, 16)) return VA_ERR_INVALID_ARG;
   for (const void* p : {(const void*)a->page_table, (const void*)a->kv_len, (const void*)a->lse,

@@ -55,6 +55,7 @@ def key_weight_args(**kw):
     (dict(flags=4), 1), (dict(flags=4, kv_scale=float("inf")), 1), (dict(scale=float("nan")), 1),
     (dict(decay=float("inf")), 1), (dict(num_pages=0), 1), (dict(max_pages=0), 1),
     (dict(num_pages=1 << 26), 2), (dict(max_pages=1 << 26), 2), (dict(B=60000, T=65, H=600), 2),
+    (dict(B=1, T=33, H=1 << 17), 2),
     (dict(q_nope=None), 1), (dict(c_kv=FAKE + 8), 1), (dict(lse=None), 1), (dict(weights=None), 1),
     (dict(tree_mask=FAKE + 4), 1), (dict(path=FAKE), 1), (dict(accept_len=FAKE), 1),
     (dict(weights_in=FAKE + 2), 1), (dict(req_status=FAKE + 1), 1),
