@@ -9,9 +9,11 @@
 // y_v is one rounding of its value, so a common r costs no accuracy.  A thread
 // holds (m, Z, S) of what it has read and rescales them once per tile of its
 // loads; two elements go through each addition and multiply-add (.f32x2).
-// Logits below -9.95e29 (masks) are read as that, so that no product overflows;
-// the rare row whose maximum is not within 9.95e29, or a scale over 1e7, is
-// summed again element by element with y_v = c (x_v - m) and eps = 0.
+// |eps| has to stay small for 2^eps to be in range: with X the power of two for
+// which 2^23 <= c X < 2^24, |eps| <= 1/2 for |m| <= X, and c X is exact.  Logits below
+// -X (masks) are read as -X, so a thread of nothing else has y_v = 0 and finite
+// sums, which its first rescaling drops.  The rare row whose maximum is not within
+// (-X, X] is summed again element by element with y_v = c (x_v - m) and eps = 0.
 //
 // Top K: a candidate is a 64-bit key, the logit in order-preserving bits over
 // the complement of its index, so that equal logits order by lower index.
@@ -25,7 +27,9 @@
 //
 // Bound by the one read of the logits from HBM; the exponentials (16 a clock
 // and SM, 11.5 logits of bf16 arrive a clock) come next.
+#include <algorithm>
 #include <cfloat>
+#include <cmath>
 #include <type_traits>
 
 #include "va_common.cuh"
@@ -42,7 +46,6 @@ constexpr int kMaxCluster = 8;
 static_assert(kMaxCluster * VA_MAX_TOPK <= kNT && kWarps * VA_MAX_TOPK <= kNT, "cut_down");
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kFloor = -1.0e4f;  // 2^kFloor = 0; keeps 0 * y finite
-constexpr float kFar = 0x1.92p99f; // the fast sums' range of the maximum: 9.95e29, a bf16 value
 
 struct LpParams {
   const void* logits;
@@ -50,6 +53,8 @@ struct LpParams {
   long long ld;
   int V, G, K;
   float scale;
+  float far;                         // X above, also as two bf16 of -X
+  uint32_t neg_far2;
   float* lse;
   float* entropy;
   float* tok_lp;
@@ -154,11 +159,11 @@ template <> struct Vec<float> {
     }
     return m;
   }
-  // the same with nothing below -kFar
-  static __device__ __forceinline__ void unpack_near(const uint4& v, float (&x)[4]) {
+  // the same with nothing below -X
+  static __device__ __forceinline__ void unpack_near(const uint4& v, const LpParams& p, float (&x)[4]) {
     unpack(v, x);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] = max_nan(x[i], -kFar);
+    for (int i = 0; i < 4; ++i) x[i] = max_nan(x[i], -p.far);
   }
 };
 template <> struct Vec<__nv_bfloat16> {
@@ -187,8 +192,8 @@ template <> struct Vec<__nv_bfloat16> {
     split(m, a, b);
     return max_nan(a, b);
   }
-  static __device__ __forceinline__ void unpack_near(const uint4& v, float (&x)[8]) {
-    constexpr uint32_t far = 0xf149f149u;  // -kFar
+  static __device__ __forceinline__ void unpack_near(const uint4& v, const LpParams& p, float (&x)[8]) {
+    const uint32_t far = p.neg_far2;
     unpack(make_uint4(max2(v.x, far), max2(v.y, far), max2(v.z, far), max2(v.w, far)), x);
   }
 };
@@ -196,7 +201,7 @@ template <> struct Vec<__nv_bfloat16> {
 // Online sums of one thread: maximum, Z and S relative to it (`Far`: of the
 // second way above).
 struct Sums {
-  float m = -kFar, z = 0.f, s = 0.f;
+  float m, z = 0.f, s = 0.f;
   template <bool Far>
   __device__ __forceinline__ void raise(float to, float c) {  // to >= m, or NaN
     const float way = Far ? (m - to) * c : __fmul_rn(m, c) - __fmul_rn(to, c);
@@ -287,7 +292,7 @@ __global__ void __launch_bounds__(kNT, 4) logprobs_kernel(const LpParams p, int 
   const int per = (nv + C - 1) / C;
   const int v0 = min(nv, (int)rank * per), v1 = min(nv, v0 + per);
   const int w0 = v0 + warp * kU * 32;      // this warp's first tile
-  const float c = p.scale * kLog2e;
+  const float c = fminf(p.scale * kLog2e, FLT_MAX);
 
   if (tid == 0) { bound = order_bits(-INFINITY); total = 0; }
   if (lane == 0) { counts[warp] = 0; kth[warp] = 0; }
@@ -336,6 +341,7 @@ __global__ void __launch_bounds__(kNT, 4) logprobs_kernel(const LpParams p, int 
   };
 
   Sums acc;
+  acc.m = -p.far;
   const uint64_t c2 = pack2(c, c);
   for (int t0 = w0; t0 < v1; t0 += kStep) {
     uint4 raw[kU];
@@ -349,7 +355,7 @@ __global__ void __launch_bounds__(kNT, 4) logprobs_kernel(const LpParams p, int 
 #pragma unroll
       for (int u = 0; u < kU; ++u) {
         float x[N];
-        VT::unpack_near(raw[u], x);
+        VT::unpack_near(raw[u], p, x);
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
           const uint64_t y2 = fma2(pack2(x[i], x[i + 1]), c2, nr2);
@@ -496,7 +502,7 @@ __global__ void __launch_bounds__(kNT, 4) logprobs_kernel(const LpParams p, int 
   float row_max = part[0];
   if (C > 1)
     for (int r = 0; r < C; ++r) row_max = max_nan(row_max, remote_f32(&part[0], r));
-  const bool far = row_max <= -kFar || (row_max > kFar && row_max < INFINITY) || p.scale > 1e7f;
+  const bool far = row_max <= -p.far || (row_max > p.far && row_max < INFINITY);
   if (far) {  // the same for all CTAs of the row: sum again, element by element
     acc.m = -FLT_MAX;
     acc.z = acc.s = 0.f;
@@ -601,6 +607,13 @@ cudaError_t launch_logprobs(const va_logprob_args& a, int sms, cudaStream_t st) 
   p.G = a.G;
   p.K = a.K;
   p.scale = a.scale;
+  // at most 2^100, where c X may be less (a scale below 2^-77)
+  int e;  // c = f 2^e, 1/2 <= f < 1
+  frexpf(std::min(a.scale * kLog2e, FLT_MAX), &e);
+  const int far_exp = std::min(24 - e, 100);
+  p.far = ldexpf(1.f, far_exp);
+  const uint32_t far_bits = (uint32_t)(127 + far_exp) << 7 | 0x8000u;
+  p.neg_far2 = far_bits << 16 | far_bits;
   p.lse = a.lse;
   p.entropy = a.entropy;
   p.tok_lp = a.tok_lp;

@@ -38,6 +38,8 @@ def check(va, t, tokens=None, k=0, scale=1.0, what=""):
 
     def same(name, a, b, grow):
         a = a.double().cpu().numpy()
+        with np.errstate(over="ignore"):  # what fp32 does not hold rounds to an infinity
+            b = np.where(np.isinf(b.astype(np.float32)), b.astype(np.float32), b)
         assert np.array_equal(np.isnan(a), np.isnan(b)), (what, name)
         assert np.array_equal(np.isneginf(a), np.isneginf(b)), (what, name)
         f = np.isfinite(b)
@@ -97,6 +99,33 @@ def test_temperature(va, scale):
     rng = np.random.default_rng(3)
     x = rng.normal(0, 2.5, (4, 9000))
     check(va, device_rows(x, "f32"), None, 4, scale=scale, what=f"scale {scale}")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [0.7, 0.9, 1.0, 1.25, 1.3, 3.0, 1e-6, 1e9])
+def test_threads_with_nothing_but_masks(va, dtype, scale):
+    """Rows shorter than the threads of a block, masks of every usual value that fill
+    whole threads, and rows that they fill, at temperatures other than one."""
+    rng = np.random.default_rng(17)
+    for V in (1, 50, 1000, 9001):
+        n = rng.normal(0, 2, V)
+        rows = [n]
+        for fill in (-1e4, -1e9, -1e20, -1e30, -np.inf):
+            rows += [np.full(V, fill), np.where(rng.random(V) < 0.97, fill, n),
+                     np.where(np.arange(V) < V // 2, fill, n)]
+        check(va, device_rows(np.stack(rows), dtype), None, min(V, 4), scale=scale,
+              what=f"{dtype} V={V} scale {scale}")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [0.9, 1.0, 1.3])
+def test_large_logits(va, dtype, scale):
+    rng = np.random.default_rng(18)
+    for V in (3, 2000):
+        n = rng.normal(0, 2, V)
+        x = np.stack([sign * 10.0 ** e + n * 10.0 ** f for e in (3, 5, 6, 7, 8, 10, 12, 20, 28, 30, 37)
+                      for sign in (1, -1) for f in (0, e - 3)])
+        check(va, device_rows(x, dtype), None, min(V, 4), scale=scale, what=f"{dtype} V={V}")
 
 
 def test_token_past_the_vocabulary_is_flagged(va):
