@@ -199,6 +199,20 @@ def test_empty_counts(va):
     near(c.run(va), c.ref())
 
 
+@pytest.mark.parametrize("dtype,kv,flags", [("bf16", "bf16", 0), ("bf16", "fp8", 0),
+                                            ("f32", "f32", 0), ("f32", "f32", 1)])
+@pytest.mark.parametrize("B,H,T,prefix", [(2, 5, 33, 700), (3, 64, 40, 300), (1, 16, 65, 2100),
+                                          (80, 8, 24, 200)])
+def test_lists_longer_than_any_path(va, dtype, kv, flags, B, H, T, prefix):
+    """T entries in any order, some more than once and some not at all: more rows than
+    the deepest path has, and than the sizes let the host expect."""
+    c = Case(B + T, B, H, T, prefix, dtype, kv)
+    c.path = c.rng.integers(0, T, (B, T)).astype(np.int32)
+    c.alen = np.full(B, T, np.int32)
+    c.alen[B // 2] = T - 1
+    near(c.run(va, flags=flags), c.ref())
+
+
 def test_same_bits_on_every_run_stream_and_replay(va):
     import torch
     c = Case(9, 2, 64, 33, (500, 77))
