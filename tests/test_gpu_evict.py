@@ -78,6 +78,18 @@ def test_longest_requests(va, cap):
                in_place=True, what=f"cap {cap}")
 
 
+@pytest.mark.parametrize("B,cap", [(80, 40000), (40, 70001), (76, 32768), (74, 9001), (30, 33000)])
+@pytest.mark.parametrize("pos", [False, True])
+def test_batches_of_long_requests(va, B, cap, pos):
+    """Clusters of one, two and four, with keys held in shared memory and read again."""
+    rng = np.random.default_rng(cap + pos)
+    w, kv_len, path, alen = make(rng, B, cap, 20)
+    w = np.round(w)  # many ties
+    at = np.stack([rng.permutation(cap) for _ in range(B)]).astype(np.int32) if pos else None
+    check_plan(va, w, kv_len, (rng.random(B) * kv_len).astype(np.int32), 20, path, alen, at, 4, 99,
+               in_place=True, what=f"{B} x {cap}")
+
+
 def test_ties_and_special_weights(va):
     """Equal weights go by slot; NaN ranks like -inf; +-0 are equal; infinities rank."""
     rng = np.random.default_rng(8)
