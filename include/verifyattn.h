@@ -436,7 +436,7 @@ size_t va_key_weights_workspace_bytes(const va_key_weight_args* args);
  * sums of three E5M2 numbers, exact to 2^-31 of a row's largest element; rows and
  * keys with an infinity or NaN give NaN.  With VA_FLAG_BF16_CUDA_CORES, of either
  * type, they run on CUDA cores.  Sums are fp32, and their order, so every bit of
- * the result, depends on sizes alone.
+ * the result, depends on the sizes, kv_len and accept_len alone.
  * req_status[b] becomes VA_ERR_INVALID_ARG when kv_len[b] is out of range
  * (the request's weights are then not written), when accept_len[b] is outside
  * [0, T] (nothing is added), or when a path entry or a page index is out of

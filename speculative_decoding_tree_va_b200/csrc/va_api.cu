@@ -406,6 +406,8 @@ int va_key_weights(const va_key_weight_args* args, va_stream_t stream) {
   p.splits = splits;
   p.scale = (args->flags & VA_FLAG_KV_FP8_E4M3) ? args->scale * args->kv_scale : args->scale;
   p.decay = args->decay;
+  p.stay = p.pass = 0;
+  if (va::kweights_on_tc(*args)) va::kweights_tc_blocks(*args, &p.stay, &p.pass);
   cudaError_t e;
   if (va::kweights_on_tc(*args)) e = va::launch_kweights_tc(*args, p, sm_count(), (cudaStream_t)stream);
   else e = va::launch_kweights_simt(*args, p, (cudaStream_t)stream);

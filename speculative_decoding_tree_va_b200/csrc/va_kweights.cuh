@@ -6,6 +6,7 @@
 #include <cuda_fp8.h>
 
 #include "va_common.cuh"
+#include "va_kweights_plan.cuh"
 
 namespace va {
 
@@ -25,9 +26,10 @@ struct KwParams {
   const int32_t* accept_len;
   const float* weights_in;
   float* weights;
-  float* part;  // [splits, B, 64 max_pages] when splits > 1
+  float* part;  // [splits, B, 64 max_pages] when splits > 1; kw_parts of them in use
   int32_t* req_status;
   int B, H, T, max_pages, num_pages, splits;
+  int stay, pass;  // tensor cores: rows that make one block, rows of a block (CUDA cores: 0)
   float scale;  // an FP8 cache's scale included
   float decay;
 };
@@ -48,6 +50,13 @@ __device__ __forceinline__ KwRequest kw_request(const KwParams& p, int b) {
   r.bad_accept = r.nodes < 0 || r.nodes > p.T;
   if (r.bad_accept) r.nodes = 0;
   return r;
+}
+
+// Partial sums that a request's keys have: on CUDA cores one from every split, on tensor
+// cores one from each part of a tile.
+__device__ __forceinline__ int kw_parts(const KwParams& p, const KwRequest& rq) {
+  if (p.pass == 0) return p.splits;
+  return kwplan::tile_parts(p.splits, kwplan::row_blocks(rq.nodes * p.H, p.stay, p.pass));
 }
 
 // Pool row of logical key `key`, -1 past kv_len or for a page outside the pool.
@@ -105,6 +114,7 @@ cudaError_t launch_kweights_join(const KwParams& p, cudaStream_t st);
 // laid out or converted first; the partial sums follow.
 bool kweights_on_tc(const va_key_weight_args& a);
 int kweights_tc_splits(const va_key_weight_args& a, int sms);
+void kweights_tc_blocks(const va_key_weight_args& a, int* stay, int* pass);
 size_t kweights_tc_workspace(const va_key_weight_args& a);
 cudaError_t launch_kweights_tc(const va_key_weight_args& a, const KwParams& p, int sms,
                                cudaStream_t st);

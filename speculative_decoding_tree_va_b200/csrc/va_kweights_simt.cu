@@ -193,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, 2) kweights_simt_kernel(const KwPara
   }
 }
 
-// Adds the splits' partial sums, in split order, to the decayed weights.
+// Adds the splits' (or parts') partial sums, in their order, to the decayed weights.
 __global__ void __launch_bounds__(64) kweights_join_kernel(const KwParams p) {
   const int b = blockIdx.y;
   const int j = blockIdx.x * 64 + threadIdx.x;
@@ -203,10 +203,11 @@ __global__ void __launch_bounds__(64) kweights_join_kernel(const KwParams p) {
   const size_t at = (size_t)b * cap + j, step = (size_t)p.B * cap;
   const float old = p.weights_in ? p.decay * p.weights_in[at] : 0.f;
   float w = 0.f;
-  for (int s0 = 0; s0 < p.splits; s0 += 8) {  // 8 loads in flight, added in order
+  const int parts = kw_parts(p, rq);
+  for (int s0 = 0; s0 < parts; s0 += 8) {  // 8 loads in flight, added in order
     float v[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) v[u] = s0 + u < p.splits ? p.part[(s0 + u) * step + at] : 0.f;
+    for (int u = 0; u < 8; ++u) v[u] = s0 + u < parts ? p.part[(s0 + u) * step + at] : 0.f;
 #pragma unroll
     for (int u = 0; u < 8; ++u) w += v[u];
   }

@@ -39,6 +39,7 @@
 // 3.2 TB/s), 16 of 4161 keys and 4160 rows 238 us (1340 TFLOP/s), 16 of 16449 FP8 keys
 // and 16 to 112 rows 69 us (2.2 TB/s), 2081 fp32 keys and 2112 rows 48 us.
 #include "va_kweights.cuh"
+#include "va_kweights_plan.cuh"
 #include "va_tc_ops.cuh"
 
 namespace va {
@@ -48,26 +49,10 @@ __device__ unsigned int g_kw_timeouts = 0;  // count of barrier waits that expir
 namespace {
 
 using namespace tc;
+using namespace kwplan;
 
-constexpr int kTileKeys = 256;        // of the pair
-constexpr int kKSlot = 128 * 128;     // bytes of a key chunk: 128 keys x 128 bytes
-constexpr int kMaxK = 12, kMaxQ = 8;  // ring slots, at most
-constexpr int kRegion = 9 * kKSlot + 9 * 64 * 128;  // keys and rows: 216 KB
 constexpr int kWarpK = 0, kWarpMma = 1, kWarpEpi = 2, kWarpQ = 10, kWarpInfo = 11;
 constexpr int kThreads = 13 * 32;     // two warps of column data
-
-enum Mode { kBf16, kFp8, kF32 };
-
-// A row's dims in chunks of 128 bytes: 8 of c_kv and one of k_pe in bf16, 4 of
-// c_kv and half a one of k_pe in FP8; planes: numbers that an element is the sum of.
-template <int M>
-struct Chunks {
-  static constexpr int n = M == kFp8 ? 5 : 9;
-  static constexpr int planes = M == kBf16 ? 1 : 3, k_planes = M == kF32 ? 3 : 1;
-  static constexpr int row_bytes = planes * (M == kFp8 ? 1 : 2) * (kDc + kDr);  // of a query row
-  static constexpr int k_slot = k_planes * kKSlot;
-  static __device__ __forceinline__ int width(int kc) { return M == kFp8 && kc == n - 1 ? 64 : 128; }
-};
 
 struct TcParams {
   KwParams k;
@@ -93,7 +78,11 @@ struct __align__(16) Ctl {
   uint64_t k_full[kMaxK], k_empty[kMaxK];
   uint64_t q_full[kMaxQ], q_empty[kMaxQ];
   uint64_t r_full;                 // rows that stay
-  uint64_t seg_done;               // a request's last tile of this pair is multiplied
+  // A request's last tile of this pair is multiplied.  Every part of a tile has a row
+  // block, so its products need loads that all four producers (keys and rows of both
+  // CTAs) issue only once they have seen the request before it end here: no phase
+  // completes before the one before it has been seen everywhere.
+  uint64_t seg_done;
   uint64_t s_full[2], s_empty[2];  // scores in tensor memory
   uint64_t i_full[2], i_empty[2];  // column data of a pass
   uint64_t drain;
@@ -122,70 +111,21 @@ __device__ __forceinline__ float ex2f(float x) {
   return y;
 }
 
-// How the rows of a request are multiplied: `blocks` passes of `cols` columns.
-// Up to kStay rows stay in shared memory: with more, fewer than 6 key chunks
-// would be in flight beside them, which HBM's latency needs (4 slots beside 256
-// rows took 8000 clocks a tile, rows through the ring 5000).
-template <int M>
-struct Shape {
-  using Ch = Chunks<M>;
-  static constexpr int kStay = M == kFp8 ? 128 : M == kF32 ? -1 : 160, kPass = M == kBf16 ? 256 : 128;
-  static constexpr int kKeySlots = M == kF32 ? 3 : Ch::n;  // when rows pass by
-  int blocks, cols;
-  bool stay;
-  __device__ __forceinline__ void set(int R) {
-    stay = R <= kStay;
-    blocks = stay ? 1 : max(1, (R + kPass - 1) / kPass);
-    cols = max(64, ((R + blocks - 1) / blocks + 63) & ~63);
-  }
-  // ring slots, and where keys and rows lie in the region
-  __device__ __forceinline__ int rows_stay() const { return cols / 2 * Ch::row_bytes; }
-  __device__ __forceinline__ int k_slots() const {
-    return stay ? min(kMaxK, (kRegion - rows_stay()) / Ch::k_slot) : kKeySlots;
-  }
-  __device__ __forceinline__ int k_at() const { return stay ? rows_stay() : 0; }
-  __device__ __forceinline__ int q_slot() const { return cols / 2 * 128 * Ch::planes; }
-  __device__ __forceinline__ int q_slots() const {
-    return min(kMaxQ, (kRegion - kKeySlots * Ch::k_slot) / q_slot());
-  }
-  __device__ __forceinline__ int q_at() const { return stay ? 0 : kKeySlots * Ch::k_slot; }
-  // Clocks of a tile, as measured: few rows wait for the keys' share of HBM, rows
-  // through the ring for its latency (5400 a pass of 192 columns, 6500 of 256).
-  __device__ __forceinline__ int cost() const {
-    const int column = M == kFp8 ? 27 : M == kF32 ? 108 : 18;
-    return stay ? max(M == kFp8 ? 3400 : 5400, column * cols + 1000)
-                : blocks * (2200 + column * cols) + 300;
-  }
-};
-
-// Tiles of a request, each in `splits` parts, and what a part costs.
-__device__ __forceinline__ int part_count(int kv_len, int splits) {
-  return (kv_len + kTileKeys - 1) / kTileKeys * splits;
-}
-template <int M>
-__device__ __forceinline__ int part_cost(const Shape<M>& sh, int splits) {
-  return max(1, sh.cost() / splits);
-}
-
 // The pair's tiles (parts of tiles), in order.  Every warp role walks them by itself.
 template <int M>
 struct Walk {
   const KwParams* p;
   long long off, end;
-  int b, tile, tiles, R, kv_len, cost;
+  int b, tile, tiles, parts, R, kv_len, cost;
   KwRequest rq;
   Shape<M> sh;
   int at, part, rb0, rb1;  // key tile, its part, and that one's row blocks
   __device__ __forceinline__ void place() {
-    at = tile;
-    part = rb0 = 0;
-    rb1 = sh.blocks;
-    if (p->splits > 1) {
-      at = tile / p->splits;
-      part = tile - at * p->splits;
-      rb0 = sh.blocks * part / p->splits;
-      rb1 = sh.blocks * (part + 1) / p->splits;
-    }
+    const Part o = part_at(tile, parts, sh.blocks);
+    at = o.at;
+    part = o.part;
+    rb0 = o.rb0;
+    rb1 = o.rb1;
   }
   __device__ __forceinline__ void load() {
     for (; b < p->B; ++b) {
@@ -196,8 +136,9 @@ struct Walk {
       kv_len = rq.kv_len;
       R = rq.nodes * p->H;
       sh.set(R);
-      tiles = part_count(kv_len, p->splits);
-      cost = part_cost(sh, p->splits);
+      parts = tile_parts(p->splits, sh.blocks);
+      tiles = part_count(kv_len, parts);
+      cost = part_cost(sh, parts);
       place();
     }
   }
@@ -297,8 +238,9 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
     auto tiles_cost = [&](const KwRequest& rq, int* tiles) {
       Shape<M> sh;
       sh.set(rq.nodes * p.H);
-      *tiles = part_count(rq.kv_len, p.splits);
-      return part_cost(sh, p.splits);
+      const int parts = tile_parts(p.splits, sh.blocks);
+      *tiles = part_count(rq.kv_len, parts);
+      return part_cost(sh, parts);
     };
     long long sum = 0;
     for (int b = b0; b < b1; ++b) {
@@ -383,7 +325,6 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
     const int oob = (F32 ? p.B * p.max_pages : p.num_pages) * kPage;  // past the pool: zeros
     for (; w.alive() && go; w.next()) {
       if (new_request(go)) ring.restart(w.sh.k_slots());
-      if (w.rb0 == w.rb1) continue;  // a part without row blocks
       const int key = w.at * kTileKeys + (int)rank * 128;
       int r0, r1;
       if (F32) {  // laid out by request and slot
@@ -512,10 +453,6 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
         const int q_slot = w.sh.q_slot(), half = w.sh.cols / 2;
         const bool seg_end = w.last_of_request();
         const Ring first = kring;  // the tile's first chunk: every block begins there
-        if (w.rb0 == w.rb1 && seg_end && ok) {  // nothing to multiply, but the request ends
-          if (elect_one()) commit_pair(&c.seg_done);
-          __syncwarp();
-        }
         for (int rb = w.rb0; rb < w.rb1 && ok; ++rb, ++pass) {
           const uint32_t d = tmem + (pass & 1) * 256;
           const bool last = rb == w.rb1 - 1;
@@ -654,7 +591,7 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
       const int P = w.kv_len - p.T;
       // a tail key is seen by some nodes only: bit n of (seen0, seen1) for node n
       const bool tail =  // of the warp
-          w.at * kTileKeys + (int)rank * 128 + 32 * q + 32 > P && w.rb0 < w.rb1;
+          w.at * kTileKeys + (int)rank * 128 + 32 * q + 32 > P;
       const int nd = key - P;
       uint64_t seen0 = ~0ull, seen1 = ~0ull;
       if (tail && nd >= 0) {
@@ -947,23 +884,11 @@ bool kweights_on_tc(const va_key_weight_args& a) {
   return a.dtype == VA_BF16 || keys * 6 * kDqk <= (1LL << 30);
 }
 
-// Parts of a tile: two of them a pair where there are fewer tiles than pairs, while
-// there are row blocks for it.  33 against 21 us for 9 tiles of 9 blocks, 53 against
-// 27 for 5 of 17, 94 against 69 for 32 of 33; with a tile a pair and more the keys'
-// second loads cost more than the even shares give (238 against 260 for 272 of 17).
-// fp32 loads the keys for every block anyway.
 int kweights_tc_splits(const va_key_weight_args& a, int sms) {
-  const int m = mode_of(a);
-  const long long rows = rows_seen(a);
-  const int stay = m == kFp8 ? Shape<kFp8>::kStay : m == kF32 ? Shape<kF32>::kStay : Shape<kBf16>::kStay;
-  const int pass = m == kBf16 ? Shape<kBf16>::kPass : Shape<kFp8>::kPass;
-  if (rows <= stay) return 1;
-  const long long blocks = (rows + pass - 1) / pass, tiles = tiles_of(a), pairs = sms / 2;
-  if (tiles >= (m == kF32 ? 8 : 1) * pairs) return 1;
-  long long s = ((m == kF32 ? 8 : 2) * pairs + tiles - 1) / tiles;
-  if (s > blocks) s = blocks;
-  if (s > VA_MAX_SPLITS) s = VA_MAX_SPLITS;
-  return s < 1 ? 1 : (int)s;
+  return plan_splits(mode_of(a), rows_seen(a), tiles_of(a), sms / 2);
+}
+void kweights_tc_blocks(const va_key_weight_args& a, int* stay, int* pass) {
+  block_rows(mode_of(a), stay, pass);
 }
 
 size_t kweights_tc_workspace(const va_key_weight_args& a) { return layout(a).total; }
