@@ -198,13 +198,20 @@ template <> struct Vec<__nv_bfloat16> {
   }
 };
 
+// c (x - m) - z for x <= m finite or -inf.  Where x - m is past fp32's range the
+// products are not both: with c x and c m each rounded it is as near, relative to itself.
+__device__ __forceinline__ float below(float x, float m, float c, float z) {
+  const float d = x - m;
+  return d == -INFINITY && x > -INFINITY ? fmaf(x, c, -fmaf(m, c, z)) : fmaf(d, c, -z);
+}
+
 // Online sums of one thread: maximum, Z and S relative to it (`Far`: of the
 // second way above).
 struct Sums {
   float m, z = 0.f, s = 0.f;
   template <bool Far>
   __device__ __forceinline__ void raise(float to, float c) {  // to >= m, or NaN
-    const float way = Far ? (m - to) * c : __fmul_rn(m, c) - __fmul_rn(to, c);
+    const float way = Far ? below(m, to, c, 0.f) : __fmul_rn(m, c) - __fmul_rn(to, c);
     const float d = max_nan(way, kFloor);
     const float f = ex2f(d);
     s = f * fmaf(z, d, s);
@@ -509,7 +516,7 @@ __global__ void __launch_bounds__(kNT, 4) logprobs_kernel(const LpParams p, int 
     for (int t0 = w0; t0 < v1; t0 += kStep)
       each_again(t0, [&](float x, int) {
         if (x > acc.m) acc.raise<true>(x, c);
-        const float y = max_nan((x - acc.m) * c, kFloor);
+        const float y = max_nan(below(x, acc.m, c, 0.f), kFloor);
         const float e = ex2f(y);
         acc.z += e;
         acc.s = fmaf(e, y, acc.s);
@@ -565,14 +572,14 @@ __global__ void __launch_bounds__(kNT, 4) logprobs_kernel(const LpParams p, int 
       lp = NAN;
       if (p.row_status) p.row_status[row] = VA_ERR_INVALID_ARG;
     } else if (t >= 0 && !none) {
-      lp = fmaf(to_f32(x0[t]) - m, p.scale, -lnz);
+      lp = below(to_f32(x0[t]), m, p.scale, lnz);
     }
     p.tok_lp[row * p.G + g] = bad ? NAN : lp;
   }
   if (tid < K) {
     const uint64_t k = cand[tid];
     const float x = order_value((uint32_t)(k >> 32));
-    float lp = none ? -INFINITY : fmaf(x - m, p.scale, -lnz);
+    float lp = none ? -INFINITY : below(x, m, p.scale, lnz);
     if (bad) lp = NAN;
     p.top_ids[row * K + tid] = bad || k == 0 ? -1 : key_index(k);
     if (p.top_lp) p.top_lp[row * K + tid] = lp;

@@ -181,3 +181,19 @@ def test_repeated_streams_and_graph(va):
     torch.cuda.synchronize()
     want = va.token_logprobs(x, k=16)
     assert all(torch.equal(p, q) for p, q in zip(r, want) if p is not None)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [0.5, 1e-20, 1e-37, 3e-38])
+def test_differences_past_the_range_of_fp32(va, dtype, scale):
+    """Logits of both signs near the type's largest, with the type's lowest beside them: their
+    difference is no fp32 number, but its scaled value is."""
+    rng = np.random.default_rng(20)
+    top = float(np.finfo(np.float32).max) if dtype == "f32" else 3.3895e38
+    for V in (4, 300, 9001):
+        u = rng.uniform(-1, 1, V) * top
+        x = np.stack([u, np.where(np.arange(V) % 2 == 0, top, -top), np.full(V, top),
+                      np.where(np.arange(V) == V // 2, 1e37, -top),
+                      np.where(rng.random(V) < 0.5, -np.inf, u)])
+        tokens = np.stack([np.arange(5) % V, np.full(5, V - 1)], 1).astype(np.int32)
+        check(va, device_rows(x, dtype), tokens, min(V, 4), scale=scale, what=f"{dtype} V={V}")
