@@ -11,9 +11,12 @@
 // loads; two elements go through each addition and multiply-add (.f32x2).
 // |eps| has to stay small for 2^eps to be in range: with X the power of two for
 // which 2^23 <= c X < 2^24, |eps| <= 1/2 for |m| <= X, and c X is exact.  Logits below
-// -X (masks) are read as -X, so a thread of nothing else has y_v = 0 and finite
-// sums, which its first rescaling drops.  The rare row whose maximum is not within
-// (-X, X] is summed again element by element with y_v = c (x_v - m) and eps = 0.
+// -X (masks, a tile's padding) are read as -X, so a thread of nothing else has y_v = 0
+// and finite sums, which its first rescaling drops, because the row's maximum is
+// at least 200 / c above: less than 2^-200 is left of them.  The rare row whose
+// maximum is nearer to -X, or above X, is summed again element by element with
+// y_v = c (x_v - m) and eps = 0; where X is the largest power taken, 2^100 (scales
+// below 2^-92), that is every row.
 //
 // Top K: a candidate is a 64-bit key, the logit in order-preserving bits over
 // the complement of its index, so that equal logits order by lower index.
@@ -45,6 +48,7 @@ constexpr int kCap = 128;    // room for them
 constexpr int kMaxCluster = 8;
 static_assert(kMaxCluster * VA_MAX_TOPK <= kNT && kWarps * VA_MAX_TOPK <= kNT, "cut_down");
 constexpr unsigned kFull = 0xffffffffu;
+constexpr float kApart = 200.f;    // binary orders from -X from which a row's maximum is not near it
 constexpr float kFloor = -1.0e4f;  // 2^kFloor = 0; keeps 0 * y finite
 
 struct LpParams {
@@ -509,7 +513,8 @@ __global__ void __launch_bounds__(kNT, 4) logprobs_kernel(const LpParams p, int 
   float row_max = part[0];
   if (C > 1)
     for (int r = 0; r < C; ++r) row_max = max_nan(row_max, remote_f32(&part[0], r));
-  const bool far = row_max <= -p.far || (row_max > p.far && row_max < INFINITY);
+  const bool far =
+      (row_max + p.far) * c < kApart || (row_max > p.far && row_max < INFINITY);
   if (far) {  // the same for all CTAs of the row: sum again, element by element
     acc.m = -FLT_MAX;
     acc.z = acc.s = 0.f;

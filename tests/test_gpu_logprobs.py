@@ -197,3 +197,29 @@ def test_differences_past_the_range_of_fp32(va, dtype, scale):
                       np.where(rng.random(V) < 0.5, -np.inf, u)])
         tokens = np.stack([np.arange(5) % V, np.full(5, V - 1)], 1).astype(np.int32)
         check(va, device_rows(x, dtype), tokens, min(V, 4), scale=scale, what=f"{dtype} V={V}")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [0.9, 1.0, 1.3, 30.0, 1e-6, 1e-28, 1e-30, 1e-36])
+def test_rows_next_to_the_lowest_logit_read_as_it_is(va, dtype, scale):
+    """The kernel reads logits below -X as -X, with X the power of two that times the scale
+    (and log2 e) is in [2^23, 2^24), or 2^100: rows whose largest logit lies from there to 300
+    binary orders of weight above, and ordinary rows where 2^100 is close to them."""
+    rng = np.random.default_rng(19)
+    c = float(np.float32(scale)) * np.log2(np.e)
+    X = 2.0 ** min(24 - np.frexp(c)[1], 100)
+    low = float(np.finfo(np.float32).min) if dtype == "f32" else -3.3895e38
+    for V in (10, 700, 9001):
+        n = np.abs(rng.normal(0, 2, V)) / c
+        n[V // 3] = 0.0
+        hide = rng.random(V) < 0.9
+        hide[V // 3] = False
+        rows = []
+        for above in (0.0, 0.5, 1.0, 8.0, 60.0, 150.0, 199.0, 201.0, 300.0):
+            x = -X + above / c - n
+            rows += [x, np.where(hide, -np.inf, x), np.where(hide, low, x),
+                     np.where(np.arange(V) == V // 3, x, -np.inf)]
+        rows += [-n, np.where(hide, -np.inf, -n), np.where(np.arange(V) == V // 3, 0.0, -np.inf)]
+        x = np.maximum(np.stack(rows), np.where(np.isneginf(np.stack(rows)), -np.inf, low))
+        check(va, device_rows(x, dtype), None, min(V, 4), scale=scale,
+              what=f"{dtype} V={V} scale {scale}")
