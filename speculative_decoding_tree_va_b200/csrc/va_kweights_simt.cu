@@ -168,6 +168,7 @@ __global__ void __launch_bounds__(kThreads, 2) kweights_simt_kernel(const KwPara
     for (int r = 0; r < 8; ++r) {
       const int rr = (r < 4 ? 0 : 60) + ty * 4 + r;
       const float l = sLse[rr];
+      if (l == INFINITY) continue;  // adds nothing, not to a key of NaN either
 #pragma unroll
       for (int c = 0; c < 8; ++c) {
         const int kk = (c < 4 ? 0 : 60) + tx * 4 + c;

@@ -3,7 +3,8 @@ a request has fewer row blocks than the call plans parts for, and many requests 
 import numpy as np
 import pytest
 
-from test_gpu_key_weights import Case, cu, near
+import _around as ar
+from test_gpu_key_weights import KINDS, Case, cu, near
 
 pytestmark = pytest.mark.gpu
 
@@ -38,3 +39,30 @@ def test_paths_shorter_than_the_plan(va, dtype, kv, B, H, T, prefix, accept):
     assert all(torch.equal(r, runs[0]) for r in runs)
     assert not status.any()
     assert va.device_timeouts() == before
+
+
+@pytest.mark.parametrize("dtype,kv,flags", KINDS)
+@pytest.mark.parametrize("H", [3, 128])
+def test_rows_that_add_nothing_meet_keys_that_are_no_numbers(va, dtype, kv, flags, H):
+    """Counted nodes that are all absent, or whose rows are all empty: a NaN or infinity in the
+    cache reaches nothing, and the old weights come back decayed."""
+    import torch
+    c = Case(31, 3, H, 9, (100, 300, 130), dtype, kv, absent=3)
+    bad = ar.slots(c.table, 0, 109)[[5, 64, 99]].tolist() + ar.slots(c.table, 1, 309)[[0, 299]].tolist()
+    for x in (c.d["c_kv"], c.d["k_pe"]):
+        if kv == "fp8":
+            x.view(torch.uint8).view(-1, x.shape[-1])[bad] = 0x7f
+        else:
+            x.view(-1, x.shape[-1])[bad] = torch.tensor([float("nan"), float("inf"), -float("inf"),
+                                                         float("nan"), float("inf")],
+                                                        device="cuda", dtype=x.dtype)[:, None]
+    c.path[0, :3], c.alen[0] = (6, 7, 8), 3          # absent nodes
+    c.path[1, :2], c.alen[1] = (0, 2), 2             # rows without a log-sum-exp
+    c.lse[1] = -np.inf
+    c.d["lse"].copy_(torch.from_numpy(c.lse))
+    old = np.abs(c.rng.normal(size=(3, c.cap))).astype(np.float32)
+    got = c.run(va, True, weights=cu(old), decay=0.5, flags=flags)
+    used = np.arange(c.cap)[None] < c.kv_len[:, None]
+    want = np.where(used, np.float32(0.5) * old, np.float32(0))
+    assert np.array_equal(got.cpu().numpy()[:2], want[:2])
+    near(got[2:], c.ref(True, old, 0.5)[2:])
