@@ -692,11 +692,13 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
   }
 }
 
-// x as the sum of three bf16 (what is left of it after two has 8 bits).
+// x as the sum of three bf16 (what is left of it after two has 8 bits); the first is
+// rounded toward zero where the nearest would be an infinity that x is not.
 __device__ __forceinline__ void split3(float x, __nv_bfloat16 (&o)[3]) {
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
     o[i] = __float2bfloat16_rn(x);
+    if (i == 0 && __hisinf(o[0])) o[0] = __float2bfloat16_rz(x);
     x -= __bfloat162float(o[i]);
   }
 }

@@ -66,3 +66,25 @@ def test_rows_that_add_nothing_meet_keys_that_are_no_numbers(va, dtype, kv, flag
     want = np.where(used, np.float32(0.5) * old, np.float32(0))
     assert np.array_equal(got.cpu().numpy()[:2], want[:2])
     near(got[2:], c.ref(True, old, 0.5)[2:])
+
+
+@pytest.mark.parametrize("flags", [0, 1])
+@pytest.mark.parametrize("H", [2, 64])
+def test_largest_finite_numbers_are_numbers(va, flags, H):
+    """fp32 elements past the largest bf16, in queries and in keys: their scores are the exact
+    ones (the other side holds 2^-123, so that a product is 32)."""
+    import torch
+    c = Case(32, 2, H, 5, (200, 77), "f32")
+    big, small = float(np.finfo(np.float32).max), 2.0 ** -123
+    sign = lambda *s: torch.from_numpy(c.rng.choice([-1.0, 1.0], s)).float()  # noqa: E731
+    n = c.c.shape[0]
+    c.qn[..., 7], c.c[..., 7] = big * sign(2, 5, H), small * sign(n, 64)
+    c.qn[..., 300], c.c[..., 300] = small * sign(2, 5, H), big * sign(n, 64)
+    c.qp[..., 63], c.k[..., 63] = big * sign(2, 5, H), small * sign(n, 64)
+    for b in range(2):
+        q, keys = c.parts(b)
+        c.lse[b] = ar.lse_ref(q, keys, c.see[b], c.prefix[b], ar.SCALE)
+    c.d.update(q_nope=c.qn.cuda(), q_pe=c.qp.cuda(), c_kv=c.c.cuda(), k_pe=c.k.cuda(),
+               lse=cu(c.lse))
+    for path in (True, False):
+        near(c.run(va, path, flags=flags), c.ref(path))
