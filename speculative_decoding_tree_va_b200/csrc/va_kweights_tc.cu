@@ -62,12 +62,17 @@ struct TcParams {
   float scale;           // k.scale, raised against the tensor cores' rounding
 };
 
-// The tensor cores' fp32 sums round toward zero at each addition, so that scores
-// come out short.  Measured over 131072 keys of one row against 64 bits, by this
-// share of the score on average: bf16 5.4e-7 to 6.1e-7 for |scores| of 3 to 30
-// (4.3e-7 below 3), FP8 1.6e-7 to 3.6e-7.  Left in, it is a common error of all
-// rows and does not average out: 3e-6 in the weights of a 4160-row request.
-constexpr double kShortBf16 = 5.2e-7, kShortFp8 = 1.8e-7;
+// The tensor cores' fp32 sums round toward zero at each addition, so that scores come
+// out short.  By this share of the score on average over the weights, measured against
+// 64 bits for mean scores of 3 to 18: bf16 and fp32 4.8e-7 to 5.4e-7, bf16 over FP8
+// 1.3e-7 to 2.0e-7, fp32 over FP8 1.0e-7 to 1.5e-7 (a code has one plane, so the
+// accumulator of the large products rounds less away).  Left in, it is a common
+// error of all rows and does not average out: 1.4e-6 of the weights at a mean score of 3,
+// 1e-5 at 18; raised by it 2e-7 and 1.5e-6.  Sums that happen to be exact come out
+// long by as much.  A bf16 verify call's own lse is short in the same way, which the
+// raise does not undo: relative to the lse it is given the weights are right, and a row's
+// add up to 1 + 1.7e-6 at a mean score of 3.
+constexpr double kShortBf16 = 5.2e-7, kShortFp8 = 1.8e-7, kShortF32Fp8 = 1.3e-7;
 
 constexpr int kBoxes = 4;  // query boxes of 8, 16, 32 or 64 rows
 struct QMaps {
@@ -905,7 +910,9 @@ cudaError_t launch_kweights_tc(const va_key_weight_args& a, const KwParams& p, i
   tp.dense = needs_rows(a);
   tp.run = tp.dense || !a.path ? 64 : a.H;
   tp.q_scale = nullptr;
-  tp.scale = (float)((double)p.scale * (1.0 + (f8 ? kShortFp8 : kShortBf16)));
+  const bool codes = a.flags & VA_FLAG_KV_FP8_E4M3;
+  tp.scale = (float)((double)p.scale *
+                     (1.0 + (!codes ? kShortBf16 : m == kF32 ? kShortF32Fp8 : kShortFp8)));
   const Layout l = layout(a);
   char* ws = static_cast<char*>(a.workspace);
   const void* qn = a.q_nope;

@@ -88,3 +88,23 @@ def test_largest_finite_numbers_are_numbers(va, flags, H):
                lse=cu(c.lse))
     for path in (True, False):
         near(c.run(va, path, flags=flags), c.ref(path))
+
+
+@pytest.mark.parametrize("dtype,kv", [("bf16", "bf16"), ("bf16", "fp8"), ("f32", "f32"), ("f32", "fp8")])
+@pytest.mark.parametrize("spread", [1.0, 3.0])
+def test_scores_are_neither_short_nor_long_on_average(va, dtype, kv, spread):
+    """Over 32768 keys of one row, the error of ln w grows with the score by at most 2.4e-7 of
+    it: 1e-7 for what the mean rounding of the sums varies by with the data, a half step of
+    fp32 (6e-8) each for the scale and its product with the cache's, 1.3e-8 for log2 e.  The
+    slope of the fit is good to 1e-8 (errors of 1.4e-6 a key, scores of 4)."""
+    import torch
+    c = Case(33, 1, 1, 1, 32767, dtype, kv)
+    for name, x in (("q_nope", c.qn), ("q_pe", c.qp)):
+        x.mul_(spread)
+        c.d[name].copy_(x)
+    c.d["lse"].zero_()
+    w = c.run(va, False)[0].double().cpu().numpy()[:32768]
+    q, keys = c.parts(0)
+    s = ar.scores_ref(q, keys, np.float64(np.float32(ar.SCALE)))[0, 0]
+    err = np.log(w) - s
+    assert abs((err * s).sum() / (s * s).sum()) <= 2.4e-7
