@@ -365,6 +365,12 @@ def _need(t, name: str, dev: int, dtype, shape) -> int:
     return t.data_ptr()
 
 
+def _axes(t, name: str, shape: str) -> None:
+    """The tensor has as many axes as `shape` names (the others' sizes are read from it)."""
+    if t.dim() != shape.count(",") + 1:
+        raise VerifyAttnError(f"{name} has shape {tuple(t.shape)}, not [{shape}]")
+
+
 class TokenLogprobs(NamedTuple):
     """What token_logprobs returns (None for what was not asked for)."""
 
@@ -456,8 +462,9 @@ def key_weights(q_nope, q_pe, c_kv, k_pe, page_table, kv_len, tree_mask, lse, *,
     [B, 64 * max_pages]; slots from kv_len on are not touched (zeros in an array
     allocated here).  out may be weights."""
     import torch
-    if q_nope.dim() != 4:
-        raise VerifyAttnError("q_nope is not [B, T, H, 512]")
+    _axes(q_nope, "q_nope", "B, T, H, 512")
+    _axes(c_kv, "c_kv", "pages, 64, 512")
+    _axes(page_table, "page_table", "B, max_pages")
     B, T, H, _ = q_nope.shape
     dev, dt, i32, f32 = q_nope.get_device(), q_nope.dtype, torch.int32, torch.float32
     if dt is not f32 and dt is not torch.bfloat16:
@@ -473,7 +480,7 @@ def key_weights(q_nope, q_pe, c_kv, k_pe, page_table, kv_len, tree_mask, lse, *,
     a.q_pe = _need(q_pe, "q_pe", dev, dt, (B, T, H, D_ROPE))
     fp8 = _fp8_cache(c_kv)
     kd = c_kv.dtype if fp8 else dt
-    n, m = c_kv.shape[0], page_table.shape[-1]
+    n, m = c_kv.shape[0], page_table.shape[1]
     a.c_kv = _need(c_kv, "c_kv", dev, kd, (n, PAGE_SIZE, D_LATENT))
     a.k_pe = _need(k_pe, "k_pe", dev, kd, (n, PAGE_SIZE, D_ROPE))
     a.page_table = _need(page_table, "page_table", dev, i32, (B, m))
@@ -578,6 +585,8 @@ def kv_move(c_kv, k_pe, page_table, from_slot, new_len, *, req_status=None, stre
     old length must be that request's alone."""
     import torch
     dev, i32 = c_kv.get_device(), torch.int32
+    _axes(c_kv, "c_kv", "pages, 64, 512")
+    _axes(page_table, "page_table", "B, max_pages")
     n, (B, m) = c_kv.shape[0], page_table.shape
     if c_kv.dtype is not torch.float32 and c_kv.dtype is not torch.bfloat16 and not _fp8_cache(c_kv):
         raise VerifyAttnError(f"c_kv is {c_kv.dtype}: not a cache type")

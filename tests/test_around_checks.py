@@ -120,3 +120,19 @@ def test_binding_refuses_host_tensors():
         va.evict_plan(f(1, 64), i(1), i(1))
     with pytest.raises(va.VerifyAttnError):
         va.kv_move(f(1, 64, 512), f(1, 64, 64), i(1, 1), i(1, 64), i(1))
+
+
+@pytest.mark.parametrize("cache,table", [((64, 512), (2, 3)), ((), (2, 3)), ((4, 64, 512), (6,)),
+                                         ((4, 64, 512), ()), ((4, 64, 512), (2, 3, 1))])
+def test_binding_refuses_other_numbers_of_axes(cache, table):
+    """A cache or page table with an axis more or less is refused by its name."""
+    import torch
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)  # noqa: E731
+    c, k, t = torch.zeros(cache), torch.zeros(4, 64, 64), i(*table) if table else i(1)[0]
+    name = "c_kv has" if len(cache) != 3 else "page_table has"
+    with pytest.raises(va.VerifyAttnError, match=name):
+        va.kv_move(c, k, t, i(2, 192), i(2))
+    q = torch.zeros(2, 1, 1, 512)
+    with pytest.raises(va.VerifyAttnError, match=name):
+        va.key_weights(q, q[..., :64], c, k, t, i(2), torch.zeros(2, 1, 1, dtype=torch.int64),
+                       torch.zeros(2, 1, 1), scale=1.0)
