@@ -190,6 +190,14 @@ typedef struct va_attn_args {
  * context stays usable.  No copy is in flight when the CTAs give up. */
 #define VA_FLAG_TEST_STALL_COPIES 8
 
+/* Test hook for va_key_weights' bounded waits (its tensor-core path only;
+ * rejected with VA_ERR_INVALID_ARG elsewhere): the kernel issues no tensor-core
+ * work, so the waits on it run into their 1 s bound.  Every request then comes
+ * back with req_status VA_ERR_CUDA and unspecified weights,
+ * va_device_timeouts() grows, and the context stays usable.  The CTAs give up
+ * long after their copies have landed. */
+#define VA_FLAG_TEST_STALL_KEY_WEIGHTS 16
+
 /* Latent cache kept as FP8 E4M3 codes, one byte per element, with one scale
  * for the whole cache: c_kv is uint8 [num_pages, 64, 512], k_pe uint8
  * [num_pages, 64, 64], and code x stands for kv_scale * value(x) in every
@@ -413,7 +421,8 @@ typedef struct va_key_weight_args {
   void* workspace;           /* [device] >= va_key_weights_workspace_bytes(),
                                 256-byte aligned                                  */
   size_t workspace_bytes;
-  int flags;                 /* VA_FLAG_BF16_CUDA_CORES, VA_FLAG_KV_FP8_E4M3      */
+  int flags;                 /* VA_FLAG_BF16_CUDA_CORES, VA_FLAG_KV_FP8_E4M3,
+                                VA_FLAG_TEST_STALL_KEY_WEIGHTS                    */
   float kv_scale;
 } va_key_weight_args;
 

@@ -110,7 +110,11 @@ int check_key_weights(const va_key_weight_args* a) {
   if (a->dtype != VA_F32 && a->dtype != VA_BF16) return VA_ERR_INVALID_ARG;
   if (a->B < 0 || a->H < 1 || a->T < 1 || a->T > VA_MAX_QLEN) return VA_ERR_INVALID_ARG;
   if (a->page_size != VA_PAGE_SIZE || a->B > VA_MAX_BATCH) return VA_ERR_UNSUPPORTED;
-  if (a->flags & ~(VA_FLAG_BF16_CUDA_CORES | VA_FLAG_KV_FP8_E4M3)) return VA_ERR_INVALID_ARG;
+  if (a->flags &
+      ~(VA_FLAG_BF16_CUDA_CORES | VA_FLAG_KV_FP8_E4M3 | VA_FLAG_TEST_STALL_KEY_WEIGHTS))
+    return VA_ERR_INVALID_ARG;
+  if ((a->flags & VA_FLAG_TEST_STALL_KEY_WEIGHTS) && !va::kweights_on_tc(*a))
+    return VA_ERR_INVALID_ARG;  // only the tensor-core kernel has the hook
   if ((a->flags & VA_FLAG_KV_FP8_E4M3) && !(a->kv_scale > 0.f && a->kv_scale <= FLT_MAX))
     return VA_ERR_INVALID_ARG;
   if (!(fabsf(a->scale) <= FLT_MAX) || !(fabsf(a->decay) <= FLT_MAX)) return VA_ERR_INVALID_ARG;

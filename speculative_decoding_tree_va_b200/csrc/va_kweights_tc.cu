@@ -60,6 +60,7 @@ struct TcParams {
   int run;               // rows that lie in order from a multiple of it on
   const float* q_scale;  // FP8 cache: [B, T H] power of two that undoes the row's
   float scale;           // k.scale, raised against the tensor cores' rounding
+  int stall;             // test hook: issue no products (the waits expire)
 };
 
 // The tensor cores' fp32 sums round toward zero at each addition, so that scores come
@@ -436,7 +437,7 @@ kweights_tc_kernel(const __grid_constant__ QMaps tm_q, const __grid_constant__ C
   } else if (warp == kWarpMma) {
     // ------------------------------------------------------------------ MMA issue
     if (rank == 0) {
-      bool ok = true;
+      bool ok = !tp.stall;
       Ring kring, qring;
       uint32_t rphase = 0, pass = 0;
       for (; w.alive() && ok; w.next()) {
@@ -913,6 +914,7 @@ cudaError_t launch_kweights_tc(const va_key_weight_args& a, const KwParams& p, i
   const bool codes = a.flags & VA_FLAG_KV_FP8_E4M3;
   tp.scale = (float)((double)p.scale *
                      (1.0 + (!codes ? kShortBf16 : m == kF32 ? kShortF32Fp8 : kShortFp8)));
+  tp.stall = (a.flags & VA_FLAG_TEST_STALL_KEY_WEIGHTS) ? 1 : 0;
   const Layout l = layout(a);
   char* ws = static_cast<char*>(a.workspace);
   const void* qn = a.q_nope;

@@ -136,3 +136,11 @@ def test_binding_refuses_other_numbers_of_axes(cache, table):
     with pytest.raises(va.VerifyAttnError, match=name):
         va.key_weights(q, q[..., :64], c, k, t, i(2), torch.zeros(2, 1, 1, dtype=torch.int64),
                        torch.zeros(2, 1, 1), scale=1.0)
+
+
+@pytest.mark.parametrize("bad", [dict(flags=17), dict(flags=17, dtype=va.VA_F32),
+                                 dict(flags=16, dtype=va.VA_F32, B=100, max_pages=100)])
+def test_the_wait_hook_is_refused_on_cuda_cores(lib, bad):
+    a = key_weight_args(**bad)
+    assert lib.va_key_weights(ctypes.byref(a), None) == va.VA_ERR_INVALID_ARG
+    assert lib.va_key_weights_workspace_bytes(ctypes.byref(a)) == 0
