@@ -2,18 +2,23 @@
 // plan (which keys stay, in which slots) and the move of one cache's keys.
 //
 // Plan.  One cluster per request; CTA r of C owns a contiguous part of the
-// slots and holds one key each in shared memory: 0 for a dropped slot, all ones
-// for a protected one, else order-preserving bits of the weight (those lie
-// strictly between).  Requests too long for that read their weights again in
-// every pass.  The k heaviest unprotected candidates are found by a radix select
-// on order-preserving bits of the weights (digits of 11, 11 and 10 bits; one
-// shared-memory histogram per CTA, joined over distributed shared memory),
-// ties by lower slot through each CTA's count of the last digit.  Kept slots
-// at or above the new length ("movers") fill the free slots below it
-// ("holes"), both in ascending order: two block scans per tile give their
-// indices, the holes are listed in the still unused end of from_slot, and
-// each mover looks its hole up.  Order-preserving compaction would move
-// every key behind the first hole; this moves only those past the new length.
+// slots.  A slot's key is 0 for a dropped slot, all ones for a protected one, else
+// order-preserving bits of the weight (those lie strictly between).  The k heaviest
+// unprotected candidates are found by a radix select on the keys (digits of 11, 11
+// and 10 bits; one shared-memory histogram per CTA, joined over distributed shared
+// memory), ties by lower slot through each CTA's count of the last digit.  Kept
+// slots at or above the new length ("movers") fill the free slots below it
+// ("holes"), both in ascending order: the holes are listed in the still unused end
+// of from_slot, and each mover looks its hole up.  Order-preserving compaction would
+// move every key behind the first hole; this moves only those past the new length.
+//
+// Parts of up to 32768 slots hold their keys in shared memory (Held): a thread takes a
+// run of up to 32 slots, one block scan of both counts gives the indices, and holes
+// and movers are listed in shared memory, in the keys' place, before they are written
+// or looked up.  Longer parts read weights and positions again for every digit and scan
+// tile by tile of four slots a thread, whose keep bits are held as a byte: batches of
+// long requests, as 64 of 131072 slots with positions (225 us; 64 of 32832, whose keys
+// are held, take 39).
 //
 // Move.  A CTA per 64 destination slots lists the slots that change and
 // copies their rows with 16-byte accesses.  No slot is both source and
@@ -34,7 +39,7 @@ constexpr int kTile = kNT * kVec;
 constexpr int kBins = 2048;
 constexpr int kBatch = 8, kFew = 4;   // loads of a thread in flight
 constexpr int kMaxKeepBytes = 128 * 1024;  // keep bits of a CTA's slots in shared memory
-constexpr int kMaxRun = 32;                // slots of a thread whose keys are held
+constexpr int kMaxRun = 32;                // slots of a thread whose keys are held, at most
 constexpr uint32_t kDropped = 0u, kProtected = ~0u;
 constexpr int kMaxCluster = 8;
 constexpr unsigned kFull = 0xffffffffu;
@@ -632,8 +637,8 @@ cudaError_t launch_evict_plan(const va_evict_args& a, int sms, cudaStream_t st) 
   p.weights_out = a.weights_out;
   p.pos_out = a.pos ? a.pos_out : nullptr;
   p.req_status = a.req_status;
-  // A request is cut over a cluster while its CTAs (one an SM) keep more than a
-  // tile each and there are SMs for them, or while their keep bits would not fit.
+  // The cluster of a request doubles while its CTAs (one an SM) have more than a tile
+  // each and twice as many still have an SM each, or while their keep bits would not fit.
   int C = 1;
   while (C < kMaxCluster &&
          ((2LL * a.B * C <= sms && (long long)a.capacity > (long long)kTile * C) ||

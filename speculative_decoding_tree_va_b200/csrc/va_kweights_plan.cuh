@@ -56,9 +56,10 @@ VA_PLAN_FN Part part_at(int t, int parts, int blocks) {
 }
 
 // How the rows of a request are multiplied: `blocks` passes of `cols` columns.
-// Up to kStay rows stay in shared memory: with more, fewer than 6 key chunks
-// would be in flight beside them, which HBM's latency needs (4 slots beside 256
-// rows took 8000 clocks a tile, rows through the ring 5000).
+// Up to kStay rows stay in shared memory.  Columns go in steps of 64: beside 192 of them 6
+// key chunks are in flight, beside 256 only 4, too few for HBM's latency (8000 clocks
+// a tile, rows through the ring 5000).  129 to 160 rows take 192 columns; 161 to 192
+// would too, but pass by, which has not been measured against it.
 template <int M>
 struct Shape {
   using Ch = Chunks<M>;
@@ -82,8 +83,11 @@ struct Shape {
     return plan_min(kMaxQ, (kRegion - kKeySlots * Ch::k_slot) / q_slot());
   }
   VA_PLAN_FN int q_at() const { return stay ? 0 : kKeySlots * Ch::k_slot; }
-  // Clocks of a tile, as measured: few rows wait for the keys' share of HBM, rows
-  // through the ring for its latency (5400 a pass of 192 columns, 6500 of 256).
+  // Clocks of a tile, for dividing the work: a fit to single tiles, few rows waiting for
+  // the keys' share of HBM and rows through the ring for its latency (5400 a pass of
+  // 192 columns, 6500 of 256).  A call takes longer than their sum over a pair (78 of
+  // 110 us, 217 of 243, 28 of 68 for the first three batches that the kernel's file
+  // names): set-up, the first loads and what a change of request drains are not in it.
   VA_PLAN_FN int cost() const {
     const int column = M == kFp8 ? 27 : M == kF32 ? 108 : 18;
     return stay ? plan_max(M == kFp8 ? 3400 : 5400, column * cols + 1000)

@@ -35,9 +35,11 @@
 // for many (128 clocks per 256 x 256 x 16; the tensor pipe is 86 % active for 4160
 // rows), in between by the latency of the rings' loads (2900 to 3600 clocks from a
 // slot's release to its refill); the exponentials take 16 a clock and SM.
-// Measured: 64 requests of 512 to 8192 keys and 64 to 576 rows 105 us (970 TFLOP/s,
-// 3.2 TB/s), 16 of 4161 keys and 4160 rows 238 us (1340 TFLOP/s), 16 of 16449 FP8 keys
-// and 16 to 112 rows 69 us (2.2 TB/s), 2081 fp32 keys and 2112 rows 48 us.
+// Measured at 1965 MHz: 64 requests of 512 to 8192 keys and 64 to 576 rows 110 us (930
+// TFLOP/s, 3.1 TB/s), 16 of 4161 keys and 4160 rows 243 us (1310 TFLOP/s), 16 of 16449
+// FP8 keys and 16 to 112 rows 68 us (2.3 TB/s), 2081 fp32 keys and 2112 rows 49 us.
+// The first two draw so much power that the clock falls to 1580 and 1395 MHz within half
+// a second of calls: 129 and 283 us then.
 #include "va_kweights.cuh"
 #include "va_kweights_plan.cuh"
 #include "va_tc_ops.cuh"

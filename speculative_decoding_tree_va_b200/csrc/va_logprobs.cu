@@ -633,8 +633,9 @@ cudaError_t launch_logprobs(const va_logprob_args& a, int sms, cudaStream_t st) 
   p.top_lp = a.top_lp;
   p.top_lp64 = a.top_lp64;
   p.row_status = a.row_status;
-  // Few rows: a row is cut over a cluster while its CTAs keep more than one
-  // tile each and the SMs do not yet hold two CTAs each.
+  // Few rows: the cluster of a row doubles while its CTAs have more than a tile each
+  // and there are fewer than two CTAs for an SM.  So a CTA keeps at least half a tile,
+  // and an SM gets fewer than four.
   const long long tile = (long long)kNT * kU * (a.dtype == VA_F32 ? 4 : 8);
   int C = 1;
   while (C < kMaxCluster && (long long)a.R * C < 2 * sms && (long long)a.V > tile * C) C *= 2;
