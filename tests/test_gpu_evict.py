@@ -233,3 +233,56 @@ def test_streams_and_graph(va):
     for b in range(B):
         at = torch.from_numpy(ar.slots(table, b, int(kv_len[b]))).cuda()
         assert torch.equal(flat[at[:n[b]]], old[at[torch.from_numpy(src[b, :n[b]]).long().cuda()]])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_weights_and_positions_through_two_steps(va, dtype):
+    """Weights, plan, move; then the next tree behind the kept keys, weights on top of the
+    plan's, and a second plan by the positions carried along: each key's weight and position
+    stay its own, whatever slot it is in."""
+    import torch
+
+    from test_gpu_key_weights import Case, near
+    B, H, T = 3, 4, 9
+    c = Case(41, B, H, T, (150, 40, 280), dtype, spare=2)
+    w1 = c.run(va, True)
+    want1 = c.ref()
+    pos = np.tile(np.arange(c.cap, dtype=np.int32), (B, 1))
+    budget = np.array([70, 30, 200], np.int32)
+    plan = va.evict_plan(w1, c.d["kv_len"], cu(budget), path=cu(c.path), accept_len=cu(c.alen),
+                         tree_len=T, pos=cu(pos), n_sink=3, n_recent=10)
+    n1, src, _, pos1, _ = ar.evict_ref(w1.cpu().numpy(), c.kv_len, budget, T, c.path, c.alen, pos, 3, 10)
+    assert np.array_equal(plan.from_slot.cpu().numpy(), src)
+    va.kv_move(c.d["c_kv"], c.d["k_pe"], c.d["page_table"], plan.from_slot, plan.new_len)
+    old = np.zeros((B, c.cap))
+    for b in range(B):
+        old[b, :n1[b]] = want1[b, src[b, :n1[b]]]
+    # the next tree: other nodes, queries and keys, behind the kept keys
+    c.prefix, c.kv_len = [int(n) for n in n1], (n1 + T).astype(np.int32)
+    c.c, c.k = c.d["c_kv"].cpu(), c.d["k_pe"].cpu()
+    for x in (c.qn, c.qp):
+        x.copy_(torch.from_numpy(c.rng.normal(size=tuple(x.shape))))
+    for b in range(B):
+        at = torch.from_numpy(ar.slots(c.table, b, int(c.kv_len[b]))[n1[b]:])
+        for pool in (c.c, c.k):
+            flat = pool.view(-1, pool.shape[-1])
+            flat[at] = torch.from_numpy(c.rng.normal(size=(T, flat.shape[1]))).to(flat.dtype)
+    c.par = ar.random_tree(c.rng, B, T)
+    c.see = ar.ancestors(c.par)
+    c.path, c.alen = ar.random_path(c.rng, c.par, c.see)
+    for b in range(B):
+        q, keys = c.parts(b)
+        c.lse[b] = ar.lse_ref(q, keys, c.see[b], c.prefix[b], ar.SCALE)
+    mask, _ = va.build_tree_mask(cu(c.par))
+    c.d.update(q_nope=c.qn.cuda(), q_pe=c.qp.cuda(), c_kv=c.c.cuda(), k_pe=c.k.cuda(),
+               kv_len=plan.new_len + T, tree_mask=mask, lse=cu(c.lse))
+    w2 = c.run(va, True, weights=plan.weights, decay=0.5, out=plan.weights)
+    want2 = c.ref()
+    for b in range(B):
+        want2[b, :c.kv_len[b]] += 0.5 * old[b, :c.kv_len[b]]
+    near(w2, want2)
+    pos2 = pos1.copy()
+    for b in range(B):
+        pos2[b, n1[b]:n1[b] + T] = 10 ** 6 + np.arange(T)
+    check_plan(va, w2.cpu().numpy(), c.kv_len, (c.kv_len // 2).astype(np.int32), T, c.path, c.alen,
+               pos2, 3, 10, in_place=True, what="second step")
