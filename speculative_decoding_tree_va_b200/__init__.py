@@ -172,7 +172,7 @@ def max_qlen() -> int:
 
 
 def device_timeouts() -> int:
-    """Expired bounded waits in the tensor-core kernel since load (synchronises)."""
+    """Expired bounded waits in the attention and key-weight kernels since load (synchronises)."""
     return int(load_library().va_device_timeouts())
 
 
